@@ -41,6 +41,11 @@ Tensor helper:
         column-major one: the call then passes the matching layout and
         transposition flags (no copy). `workspace` (a CUDA tensor) enables the
         stream-K kernels (sgemm_f32_ws).
+
+The gated feed-forward block, its backward pass and products with 4-bit
+weights (float32, bfloat16, float16; include/sgemm_f32_ffn.h) are bound in
+ffn.py and exported here: glu, glu_backward, w4_quantize, w4_dequantize,
+w4_matmul, w4_glu, and the sgemm_f32_glu* and sgemm_f32_w4* mirrors.
 """
 from __future__ import annotations
 
@@ -443,3 +448,10 @@ def gemm(A, B, C, alpha: float = 1.0, beta: float = 0.0, variant=None, stream=No
     if rc != 0:
         raise SgemmError(rc, where)
     return C
+
+
+# The gated feed-forward block and 4-bit weights (ffn.py binds their entry
+# points of the same library).
+from .ffn import (ACTS, W4, glu, glu_backward, glu_backward_workspace, sgemm_f32_glu,  # noqa: E402,F401
+                  sgemm_f32_glu_bwd, sgemm_f32_glu_bwd_ws_size, sgemm_f32_w4, sgemm_f32_w4_dequantize,
+                  sgemm_f32_w4_glu, sgemm_f32_w4_quantize, w4_dequantize, w4_glu, w4_matmul, w4_quantize)

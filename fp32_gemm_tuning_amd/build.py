@@ -27,7 +27,8 @@ LIB = os.path.join(PKG, "libsgemm_f32.so")
 ARCH = os.environ.get("SGEMM_F32_ARCH", "gfx950")
 
 SOURCES = ["api.hip", "ladder.hip", "valu_main.hip", "mfma_pipe.hip", "mfma_kgroup.hip",
-           "mfma_small.hip", "peak.hip"]
+           "mfma_small.hip", "peak.hip", "ffn_api.hip", "glu_tile.hip", "glu_grad.hip", "w4.hip",
+           "w4_pack.hip"]
 
 CXXFLAGS = [
     f"--offload-arch={ARCH}",

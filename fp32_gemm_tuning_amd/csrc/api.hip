@@ -552,23 +552,45 @@ SGEMM_F32_API const char* sgemm_f32_strerror(int code) {
     switch (code) {
         case 0: return "success";
         case -1: return "argument 1 (M) is negative";
-        case -2: return "argument 2 (N) is negative";
+        case -2: return "argument 2 (N, or F) is negative";
         case -3: return "argument 3 (K) is negative";
-        case -5: return "argument 5 (A) is NULL or not 4-byte aligned";
-        case -6: return "argument 6 (lda) is smaller than the contiguous extent of A as stored "
+        case -5: return "argument 5 (A; X or W) is NULL or not aligned to its element";
+        case -6: return "argument 6 (lda; ldx, ldw) is smaller than the contiguous extent of A as stored "
                         "(max(1, K) for row-major, untransposed A)";
-        case -7: return "argument 7 (B) is NULL or not 4-byte aligned";
-        case -8: return "argument 8 (ldb) is smaller than the contiguous extent of B as stored "
+        case -7: return "argument 7 (B; Wg, Q) is NULL or not aligned to its element";
+        case -8: return "argument 8 (ldb; ldwg, ldq) is smaller than the contiguous extent of B as stored "
                         "(max(1, N) for row-major, untransposed B)";
-        case -10: return "argument 10 (C) is NULL or not 4-byte aligned";
-        case -11: return "argument 11 (ldc) is smaller than the contiguous extent of C "
+        case -10: return "argument 10 (C; H, Y, W) is NULL or not aligned to its element";
+        case -11: return "argument 11 (ldc; ldh, ldy, ldw) is smaller than the contiguous extent of C "
                          "(max(1, N) row-major, max(1, M) column-major)";
         case -12: return "output pointer is NULL";
         case -13: return "layout is neither SGEMM_F32_ROW_MAJOR nor SGEMM_F32_COL_MAJOR";
         case -14: return "transa is neither SGEMM_F32_NO_TRANS nor SGEMM_F32_TRANS";
         case -15: return "transb is neither SGEMM_F32_NO_TRANS nor SGEMM_F32_TRANS";
         case -16: return "workspace is NULL with a nonzero size, or not 16-byte aligned";
-        case SGEMM_F32_ERR_WORKSPACE: return "the stream-K variant needs a larger workspace (sgemm_f32_ws_size)";
+        case -17: return "dtype is not one of SGEMM_F32_DTYPE_*";
+        case -18: return "act is not one of SGEMM_F32_ACT_*";
+        case -19: return "Wu (Qu) is NULL or misaligned";
+        case -20: return "ldwu is smaller than max(1, K)";
+        case -21: return "P is NULL or not 4-byte aligned";
+        case -22: return "ldp is smaller than max(1, 2F)";
+        case -23: return "dH is NULL or misaligned";
+        case -24: return "lddh is smaller than max(1, F)";
+        case -25: return "dX is misaligned";
+        case -26: return "lddx is smaller than max(1, K)";
+        case -27: return "dWg is misaligned";
+        case -28: return "lddwg is smaller than max(1, K)";
+        case -29: return "dWu is misaligned";
+        case -30: return "lddwu is smaller than max(1, K)";
+        case -31: return "group is neither a positive multiple of 32 nor at least K";
+        case -32: return "the scales (Sg) are NULL or misaligned";
+        case -33: return "lds is smaller than the number of groups";
+        case -34: return "the zero points (Zg) are misaligned";
+        case -35: return "ldz is smaller than the number of groups";
+        case -36: return "Su is NULL or misaligned";
+        case -37: return "Zu is misaligned, or only one of Zg and Zu is NULL";
+        case SGEMM_F32_ERR_WORKSPACE: return "the workspace is smaller than the call needs "
+                                             "(sgemm_f32_ws_size, sgemm_f32_glu_bwd_ws_size)";
         case SGEMM_F32_ERR_SCRATCH: return "the stream-K variant needs more workspace than the "
                                            "library's fixed scratch holds (SGEMM_F32_SCRATCH_BYTES)";
         case SGEMM_F32_ERR_VARIANT: return "variant id out of range";

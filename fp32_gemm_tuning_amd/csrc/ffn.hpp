@@ -1,0 +1,144 @@
+// Shared pieces of the gated feed-forward and 4-bit kernels
+// (include/sgemm_f32_ffn.h): the element types, the gate's activations, the
+// argument blocks and the launchers that ffn_api.hip calls.
+#pragma once
+
+#include "kernels.hpp"
+
+#include <type_traits>
+
+#include "sgemm_f32_ffn.h"
+
+namespace sgemm {
+
+typedef __bf16 bf16;
+typedef _Float16 f16;
+
+// f(type tag) with the call's element type; the tag's ::type is float, bf16
+// or f16.
+template <class T>
+struct TypeTag {
+    using type = T;
+};
+template <class Fn>
+static inline hipError_t with_dtype(int dtype, Fn&& f) {
+    if (dtype == SGEMM_F32_DTYPE_F32) return f(TypeTag<float>{});
+    if (dtype == SGEMM_F32_DTYPE_BF16) return f(TypeTag<bf16>{});
+    return f(TypeTag<f16>{});
+}
+static inline int64_t dtype_bytes(int dtype) { return dtype == SGEMM_F32_DTYPE_F32 ? 4 : 2; }
+
+// Activations and their slopes, in FP32. Each form stays finite and keeps its
+// limit where an intermediate overflows: exp(-g) = inf gives -0 for a large
+// negative g, and a slope's second term, whose factor has underflowed to 0,
+// is dropped rather than multiplied by a large g.
+__device__ __forceinline__ float act_value(int act, float g) {
+    switch (act) {
+        case SGEMM_F32_ACT_SILU: return g / (1.0f + expf(-g));
+        case SGEMM_F32_ACT_GELU: return 0.5f * g * erfcf(-0.70710678118654752f * g);
+        case SGEMM_F32_ACT_GELU_TANH: {
+            const float v = 0.79788456080286536f * (g + 0.044715f * g * g * g);
+            return g / (1.0f + expf(-2.0f * v));   // (1 + tanh v) / 2 = 1 / (1 + exp(-2v))
+        }
+        default: return g < 0.0f ? 0.0f : g;       // NaN stays NaN
+    }
+}
+__device__ __forceinline__ float act_slope(int act, float g) {
+    switch (act) {
+        case SGEMM_F32_ACT_SILU: {
+            const float s = 1.0f / (1.0f + expf(-g)), t = s * (1.0f - s);
+            return t == 0.0f ? s : s + g * t;
+        }
+        case SGEMM_F32_ACT_GELU: {
+            const float cdf = 0.5f * erfcf(-0.70710678118654752f * g);
+            const float pdf = 0.39894228040143268f * expf(-0.5f * g * g);
+            return pdf == 0.0f ? cdf : cdf + g * pdf;
+        }
+        case SGEMM_F32_ACT_GELU_TANH: {
+            const float v = 0.79788456080286536f * (g + 0.044715f * g * g * g);
+            const float s = 1.0f / (1.0f + expf(-2.0f * v)), t = s * (1.0f - s);
+            return t == 0.0f ? s
+                             : s + g * t * (2.0f * 0.79788456080286536f) * (1.0f + 0.134145f * g * g);
+        }
+        default: return g > 0.0f ? 1.0f : (g != g ? g : 0.0f);
+    }
+}
+
+// One forward call of the gated block: H = act(X Wg^T) * (X Wu^T), and the
+// pre-activations in P where it is not null.
+struct GluArgs {
+    const void* X;
+    const void* Wg;
+    const void* Wu;
+    void* H;
+    float* P;
+    int64_t ldx, ldwg, ldwu, ldh, ldp;
+    int32_t M, F, K;
+    int32_t act;
+};
+
+// The elementwise step of the backward pass: dG and dU (M x F in the type,
+// leading dimension ldd, columns F .. ldd-1 written as zero) from P and dH.
+struct GluGradArgs {
+    const float* P;
+    const void* dH;
+    void* dG;
+    void* dU;
+    int64_t ldp, lddh, ldd;
+    int32_t M, F;
+    int32_t act;
+};
+
+// A 16-bit product of the backward pass. dX: C0 = dG W[0] + dU W[1]; dW:
+// C0 = dG^T X, C1 = dU^T X (either may be null). D are dG and dU (M x F,
+// leading dimension ldd).
+struct GluProdArgs {
+    const void* D[2];
+    const void* W[2];
+    const void* X;
+    void* C[2];
+    int64_t ldd, ldw[2], ldx, ldc[2];
+    int32_t M, F, K;
+};
+
+// A call over 4-bit weights: one matrix (w4) or two (w4_glu).
+struct W4Args {
+    const void* X;
+    const uint8_t* Q[2];
+    const void* S[2];
+    const void* Z[2];
+    void* Y;
+    int64_t ldx, ldq, lds, ldz, ldy;
+    int32_t M, F, K;
+    int32_t group;
+    int32_t act;
+};
+
+struct PackArgs {
+    const void* W;   // the matrix quantised; dequantisation writes it
+    uint8_t* Q;
+    void* S;
+    void* Z;
+    int64_t ldw, ldq, lds, ldz;
+    int32_t F, K;
+    int32_t group;
+};
+
+// glu_tile.hip
+int check_glu(const GluArgs& a);
+hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s);
+int check_glu_prod(const GluProdArgs& a);
+hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s);
+hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s);
+// glu_grad.hip
+int check_glu_grad(const GluGradArgs& a);
+hipError_t launch_glu_grad(int dtype, const GluGradArgs& a, hipStream_t s);
+// w4.hip
+int check_w4(const W4Args& a, bool dual);
+hipError_t launch_w4(int dtype, const W4Args& a, bool dual, hipStream_t s);
+// w4_pack.hip
+int check_w4_pack(const PackArgs& a);
+hipError_t launch_w4_quantize(int dtype, const PackArgs& a, hipStream_t s);
+hipError_t launch_w4_dequantize(int dtype, const PackArgs& a, hipStream_t s);
+
+}  // namespace sgemm
