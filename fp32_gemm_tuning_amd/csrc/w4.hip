@@ -12,10 +12,9 @@
 // bfloat16 parts that add up to them exactly (8 + 8 + 8 bits), so each
 // product is exact in every type.
 #include "ffn.hpp"
+#include "mfma_pipecore.hpp"   // ring_barrier
 
 namespace sgemm {
-
-static inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef i32x4 i32x4_u1 __attribute__((aligned(1)));
@@ -50,26 +49,34 @@ struct W4Type<f16> {
 
 // Eight stored numbers to eight 16 + q. Pair e of the result holds numbers e
 // and e + 4, so the activations are paired the same way (pair_up).
+// The two constants come from registers the compiler cannot see through: one
+// and-or instruction takes a scalar and a vector register, not two literals.
 template <class T>
-__device__ __forceinline__ i32x4 unpack(uint32_t w) {
-    using C = W4Type<T>;
-    i32x4 r;
+struct Unpack {
+    uint32_t mask = W4Type<T>::MASK, base = W4Type<T>::BASE;
+    __device__ __forceinline__ Unpack() { asm("" : "+s"(mask), "+v"(base)); }
+    __device__ __forceinline__ i32x4 operator()(uint32_t w) const {
+        i32x4 r;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int left = C::SHIFT - 4 * e;
-        r[e] = (int)(((left >= 0 ? w << left : w >> -left) & C::MASK) | C::BASE);
+        for (int e = 0; e < 4; ++e) {
+            const int left = W4Type<T>::SHIFT - 4 * e;
+            r[e] = (int)(((left >= 0 ? w << left : w >> -left) & mask) | base);
+        }
+        return r;
     }
-    return r;
-}
+};
 
 // Eight consecutive activations of a row, as loaded.
 template <class T>
 struct XRaw {
     i32x4 v[sizeof(T) / 2];
-    // `left` elements of the row remain at p; those past them are zero.
-    __device__ __forceinline__ void load(const T* p, int left) {
-        typedef i32x4 V __attribute__((aligned(2)));
-        if (left >= 8) {
+    // Elements at .. at + 7 of a row of n elements; place() zeroes those past
+    // its end. Apart, and without branches, as load_w32.
+    template <bool RAGGED>   // else all 8 exist, or none
+    __device__ __forceinline__ void fetch(const T* row, int at, int n) {
+        if constexpr (!RAGGED) {
+            typedef i32x4 V __attribute__((aligned(2)));
+            const T* p = row + (at < n ? at : 0);
 #pragma unroll
             for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = ((const V*)p)[i];
         } else {
@@ -77,15 +84,44 @@ struct XRaw {
             typedef T E __attribute__((ext_vector_type(EPV)));
 #pragma unroll
             for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-                E x = __builtin_bit_cast(E, i32x4{0, 0, 0, 0});
+                E x;
 #pragma unroll
-                for (int e = 0; e < EPV; ++e)
-                    if (i * EPV + e < left) x[e] = p[i * EPV + e];
+                for (int e = 0; e < EPV; ++e) {
+                    const int k = at + i * EPV + e;
+                    x[e] = row[k < n ? k : n - 1];
+                }
                 v[i] = __builtin_bit_cast(i32x4, x);
             }
         }
     }
+    template <bool RAGGED>
+    __device__ __forceinline__ void place(int at, int n) {
+        constexpr int EPV = 16 / sizeof(T);
+        typedef T E __attribute__((ext_vector_type(EPV)));
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            E x = __builtin_bit_cast(E, v[i]);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e)
+                if (at + (RAGGED ? i * EPV + e : 0) >= n) x[e] = (T)0.0f;
+            v[i] = __builtin_bit_cast(i32x4, x);
+        }
+    }
 };
+
+// 16 bytes (32 numbers) of a row of at least 16 bytes, from byte `at`: load_w32
+// reads the last 16 where these would reach past the row's end, and place_w32
+// shifts them down. (Numbers past the row's end meet activations that are
+// zero.) Apart, so that many loads are in flight: a load whose value is used
+// in a branch is waited for there.
+__device__ __forceinline__ i32x4 load_w32(const uint8_t* row, int at, int bytes) {
+    return *(const i32x4_u1*)(row + (at < bytes - 16 ? at : bytes - 16));
+}
+__device__ __forceinline__ i32x4 place_w32(const i32x4& v, int at, int bytes) {
+    const int past = at - (bytes - 16);
+    const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, v);
+    return __builtin_bit_cast(i32x4, x >> (past <= 0 ? 0 : past < 16 ? 8 * past : 120));
+}
 
 // Halves of two words: the low or the high ones, a's first.
 __device__ __forceinline__ int lows(int a, int b) {
@@ -117,6 +153,231 @@ __device__ __forceinline__ void pair_up(const XRaw<float>& x, i32x4 (&p)[3]) {
     }
 }
 
+// Groups along k, in steps of 32: `steps` to a group, `shift` its logarithm or
+// -1.
+struct W4Groups {
+    int steps, shift;
+    __device__ __forceinline__ int of(int step) const { return shift >= 0 ? step >> shift : step / steps; }
+};
+
+// ---------------------------------------------------------------------------
+// Few rows of X: vector units.
+//
+// A lane owns 32 consecutive k of every weight row, one 16-byte load, so a wave
+// reads a row's 1 KiB in one piece, and a group's scale one element per lane, next
+// to its neighbours'. The lane's activations stay in registers while it walks the
+// rows. All of a wave's loads go out before its first product: with a
+// launch that fills the chip once there is no loop to overlap them in.
+// ---------------------------------------------------------------------------
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float dot2(bf16, int a, int b, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+}
+__device__ __forceinline__ float dot2(f16, int a, int b, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c, false);
+}
+
+// A lane's 32 activations of one row and their sum.
+template <class T>
+struct LaneX {
+    i32x4 p[4];   // paired as the numbers unpack
+    float sum;
+    __device__ __forceinline__ void set(const XRaw<T> (&r)[4]) {
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            i32x4 one[1];
+            pair_up(r[j], one);
+            p[j] = one[0];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum = dot2(T{}, p[j][e], (int)W4Type<T>::ONES, sum);
+        }
+    }
+    // sum (16 + q) x, less 16 sum x with the zero point's part.
+    __device__ __forceinline__ float times(const Unpack<T>& unpack, const i32x4& w, float z) const {
+        float v[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const i32x4 u = unpack((uint32_t)w[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e & 1] = dot2(T{}, p[j][e], u[e], v[e & 1]);
+        }
+        return __builtin_fmaf(-(16.0f + z), sum, v[0] + v[1]);
+    }
+};
+template <>
+struct LaneX<float> {
+    float x[32];
+    float sum;
+    __device__ __forceinline__ void set(const XRaw<float> (&r)[4]) {
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f32x4 a = __builtin_bit_cast(f32x4, r[j].v[0]), b = __builtin_bit_cast(f32x4, r[j].v[1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[8 * j + e] = a[e];
+                x[8 * j + 4 + e] = b[e];
+                sum += a[e] + b[e];
+            }
+        }
+    }
+    __device__ __forceinline__ float times(const Unpack<float>&, const i32x4& w, float z) const {
+        float v[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e & 1] = __builtin_fmaf((float)(((uint32_t)w[j] >> (4 * e)) & 15), x[8 * j + e], v[e & 1]);
+        return __builtin_fmaf(-z, sum, v[0] + v[1]);
+    }
+};
+
+// The sums of four values over a wave's lanes: quarter i of the result (lanes
+// 16 i ..) holds the sum of value i. Two lane swaps halve four values to one,
+// and a row of 16 lanes is summed by data-parallel moves (a shuffle through LDS
+// for each value and step cost more than the products).
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+    const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true);
+    return v + __builtin_bit_cast(float, o);
+}
+__device__ __forceinline__ float add_halves(float a, float b) {   // a in lanes 0-31, b in 32-63
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a),
+                                                    __builtin_bit_cast(uint32_t, b), false, false);
+    return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+__device__ __forceinline__ float add_rows(float a, float b) {     // a in even rows of 16, b in odd ones
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a),
+                                                    __builtin_bit_cast(uint32_t, b), false, false);
+    return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+__device__ __forceinline__ float wave_sums(float a, float b, float c, float d) {
+    float v = add_rows(add_halves(a, c), add_halves(b, d));
+    v = add_dpp<0xB1>(v);    // quad_perm 1,0,3,2
+    v = add_dpp<0x4E>(v);    // quad_perm 2,3,0,1
+    v = add_dpp<0x141>(v);   // row_half_mirror
+    return add_dpp<0x140>(v);   // row_mirror
+}
+
+// kw waves share the k of a row (64 lanes of 32 each) and add up in wave
+// order; blockDim.x / (64 kw) such sets take RW features each.
+template <class T, bool DUAL, int MR, bool RAGGED>
+__global__ __launch_bounds__(512) void k_w4_few(W4Args a, W4Groups gr, int kw) {
+    constexpr int D = DUAL ? 2 : 1, RW = DUAL ? 4 : 8;
+    constexpr int N = D * RW * MR;   // sums per wave, value (d, r, m) at (d * RW + r) * MR + m
+    __shared__ float red[8][N];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int set = w / kw, kp = w - set * kw, sets = (blockDim.x >> 6) / kw;
+    const int f0 = (blockIdx.x * sets + set) * RW;
+    const int bytes = (a.K + 1) / 2;
+    const bool zeros = a.Z[0] != nullptr;
+    const Unpack<T> unpack;
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+
+    for (int kb = kp * 2048; kb < a.K; kb += kw * 2048) {
+        const int k = kb + lane * 32, at = k >> 1;
+        const int step = k >> 5, last = (a.K - 1) >> 5;
+        const int g = gr.of(step < last ? step : last);
+        XRaw<T> x[MR][4];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            const T* row = (const T*)a.X + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[m][j].template fetch<RAGGED>(row, k + 8 * j, a.K);
+        }
+        // Row by row, so that the first rows' products run while the last ones'
+        // weights arrive. Without zero points the scale is read twice and the
+        // second value ignored (a load on some paths only would be waited
+        // for with all before it).
+        i32x4 q[D][RW];
+        T s[D][RW], z[D][RW];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const int64_t f = f0 + r < a.F ? f0 + r : a.F - 1;
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                q[d][r] = load_w32(a.Q[d] + f * a.ldq, at, bytes);
+                s[d][r] = ((const T*)a.S[d])[f * a.lds + g];
+                z[d][r] = ((const T*)(zeros ? a.Z[d] : a.S[d]))[f * (zeros ? a.ldz : a.lds) + g];
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        LaneX<T> lx[MR];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[m][j].template place<RAGGED>(k + 8 * j, a.K);
+            lx[m].set(x[m]);
+        }
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const i32x4 w32 = RAGGED ? place_w32(q[d][r], at, bytes) : q[d][r];
+                const float zp = zeros ? (float)z[d][r] : 8.0f;
+#pragma unroll
+                for (int m = 0; m < MR; ++m) {
+                    float& o = acc[(d * RW + r) * MR + m];
+                    o = __builtin_fmaf((float)s[d][r], lx[m].times(unpack, w32, zp), o);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float v = wave_sums(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        if ((lane & 15) == 0) red[w][i + (lane >> 4)] = v;
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < sets * RW * MR) {
+        const int m = t % MR, r = (t / MR) % RW, st = t / (MR * RW);
+        const int f = (blockIdx.x * sets + st) * RW + r;
+        float v[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            for (int i = 0; i < kw; ++i) v[d] += red[st * kw + i][(d * RW + r) * MR + m];
+        if (m < a.M && f < a.F)
+            ((T*)a.Y)[(int64_t)m * a.ldy + f] = (T)(DUAL ? act_value(a.act, v[0]) * v[1] : v[0]);
+    }
+}
+
+template <class T, bool DUAL, int MR>
+static hipError_t launch_few(const W4Args& a, const W4Groups& gr, hipStream_t s) {
+    const int64_t need = cdiv(a.K, 2048);
+    const int kw = need < 1 ? 1 : need > 8 ? 8 : (int)need;
+    const int sets = kw >= 4 ? 1 : 4 / kw;
+    const dim3 grid((unsigned)cdiv(a.F, sets * (DUAL ? 4 : 8)));
+    if (a.K % 32 != 0)
+        hipLaunchKernelGGL((k_w4_few<T, DUAL, MR, true>), grid, dim3(64 * kw * sets), 0, s, a, gr, kw);
+    else
+        hipLaunchKernelGGL((k_w4_few<T, DUAL, MR, false>), grid, dim3(64 * kw * sets), 0, s, a, gr, kw);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// More rows: matrix cores.
+//
+// A workgroup's eight waves are two streams of 16 weight rows (32 features, or
+// the two matrices' rows of 16 features) by four runs of 128 k, so one pass of its loop
+// covers 512 k. X's part of a pass is staged in LDS once for both streams,
+// already paired (and split, for FP32), as 16-byte units [part][k / 8][row],
+// the operand of lane (k / 8 % 4, row) of the 16x16x32 matrix instruction.
+// Memory is read along the rows, consecutive lanes on consecutive 16 bytes, and
+// rearranged through LDS: read in operand order, where neighbouring
+// lanes take different rows, each load instruction touched 16 lines and took
+// four times as long. A weight row's words reach their step's lanes by a 4 x 4
+// transpose between words and quarters of the wave, which puts 32
+// consecutive k in each step, so any group of whole steps is scaled apart: PER
+// steps of a run share their scales.
+// ---------------------------------------------------------------------------
+
 // The 4 x 4 transpose between a lane's four words and the four quarters of
 // the wave: word j of quarter q and word q of quarter j change places.
 __device__ __forceinline__ void transpose4(i32x4& d) {
@@ -127,235 +388,220 @@ __device__ __forceinline__ void transpose4(i32x4& d) {
     d = i32x4{(int)c[0], (int)c[1], (int)e[0], (int)e[1]};
 }
 
-// Groups along k, in steps of 32: `steps` to a group (`shift` its logarithm, or
-// -1), and `per` steps of a block of four between two uses of the scales.
-struct W4Groups {
-    int steps, shift, per;
-};
-
-// A workgroup takes 16 MB rows of X and 16 NB output features; its NW waves take
-// blocks of 128 k in turn and their sums are added in wave order at the end.
-// Per block a lane loads 16 bytes (32 numbers) of row lane % 16 of each 16
-// features, so a row's four lanes read 64 contiguous bytes; the transpose then
-// gives step j of the block the numbers k = 32 j + 8 (lane / 16) + 0..7, which is
-// the operand layout of the 16x16x32 matrix instruction, and any group of
-// whole steps can be scaled apart. X's operands come straight from memory
-// (the cache holds them: X is small beside the weights).
-template <class T, bool DUAL, int MB, int NB, int NW>
-__global__ __launch_bounds__(NW * 64) void k_w4(W4Args a, W4Groups gr) {
+template <class T, bool DUAL, int MB, int PER>
+__global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
     using C = W4Type<T>;
-    constexpr int D = DUAL ? 2 : 1;
-    __shared__ float red[NW][D][MB][4][68];
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    constexpr int ROWS = 16 * MB, UNITS = 64 * ROWS;   // 16-byte units of a part's pass
+    constexpr int XI = ROWS / 8;                       // units per thread
+    __shared__ i32x4 xs[2][C::PARTS * UNITS];
+    __shared__ i32x4 ws[8][64];
+    __shared__ float sc[2][2][32][17];   // [stage][scale, 16 + zero point][row][step]
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
     const int q = lane >> 4, c = lane & 15;
-    const int f0 = blockIdx.x * (16 * NB), m0 = blockIdx.y * (16 * MB);
-    const int bytes = (a.K + 1) / 2;
-    const int nblk = (a.K + 127) / 128;
-
-    // Rows past the last one repeat it; their results are not stored.
-    const T* xrow[MB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-        const int m = m0 + 16 * i + c;
-        xrow[i] = (const T*)a.X + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
-    }
-    const uint8_t* wrow[D][NB];
-    const T* srow[D][NB];
-    const T* zrow[D][NB];
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const int f = f0 + 16 * n + c;
-            const int64_t r = f < a.F ? f : a.F - 1;
-            wrow[d][n] = a.Q[d] + r * a.ldq;
-            srow[d][n] = (const T*)a.S[d] + r * a.lds;
-            zrow[d][n] = (const T*)a.Z[d] + r * a.ldz;
-        }
+    const int stream = w & 1, run = w >> 1;
+    const int f0 = blockIdx.x * (DUAL ? 16 : 32), m0 = blockIdx.y * ROWS;
+    const int bytes = (a.K + 1) / 2, passes = (a.K + 511) / 512;
     const bool zeros = a.Z[0] != nullptr;
 
-    struct Blk {
-        i32x4 w[D][NB];
-        T s[D][NB][4], z[D][NB][4];
+    // What this thread loads: its weight row (of its stream), its scale's row
+    // and its rows of X. Rows past the last repeat it; their results are not stored.
+    auto feature = [&](int r) { return DUAL ? f0 + (r & 15) : f0 + r; };   // of row r of 32
+    auto matrix = [&](int r) { return DUAL ? r >> 4 : 0; };
+    auto clampf = [&](int f) { return (int64_t)(f < a.F ? f : a.F - 1); };
+    const int wr = 16 * stream + (lane >> 2);
+    const uint8_t* wrow = a.Q[DUAL ? stream : 0] + clampf(feature(wr)) * a.ldq;
+    const int sr = t >> 4, ss = t & 15;
+    const int sd = matrix(sr);
+    const T* srow = (const T*)(sd ? a.S[1] : a.S[0]) + clampf(feature(sr)) * a.lds;
+    // (without zero points the scale is read again and ignored)
+    const T* zrow = zeros ? (const T*)(sd ? a.Z[1] : a.Z[0]) + clampf(feature(sr)) * a.ldz : srow;
+    const int last_step = (a.K - 1) >> 5;
+
+    struct Ahead {   // one pass's weights and scales, on their way
+        i32x4 w;
+        T s, z;
     };
-    auto load = [&](int b, Blk& r) {
-        const int at = 64 * b + 16 * q;
-        const bool whole = 64 * b + 64 <= bytes;
+    auto load_ahead = [&](int p, Ahead& r) {
+        const int at = 256 * p + 64 * run + 16 * (lane & 3);
+        if (bytes >= 16) {
+            r.w = load_w32(wrow, at, bytes);
+        } else {
+            unsigned __int128 x = 0;
+            for (int i = 0; at + i < bytes; ++i) x |= (unsigned __int128)wrow[at + i] << (8 * i);
+            r.w = __builtin_bit_cast(i32x4, x);
+        }
+        const int st = 16 * p + ss, g = gr.of(st < last_step ? st : last_step);
+        r.s = srow[g];
+        r.z = zrow[g];
+    };
+    struct XPass {
+        XRaw<T> r[XI];
+    };
+    auto load_x = [&](int p, XPass& x) {
+        const int k = 512 * p + 8 * lane;
 #pragma unroll
-        for (int d = 0; d < D; ++d)
+        for (int i = 0; i < XI; ++i) {
+            const int m = m0 + w + 8 * i;
+            const T* row = (const T*)a.X + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
+            if (a.K % 8 == 0 || 512 * p + 512 <= a.K)
+                x.r[i].template fetch<false>(row, k, a.K);
+            else
+                x.r[i].template fetch<true>(row, k, a.K);
+        }
+    };
+    auto store_x = [&](int p, XPass& x) {
+        const int k = 512 * p + 8 * lane;
+        i32x4* st = xs[p & 1];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const uint8_t* p = wrow[d][n] + at;
-                if (whole) {
-                    r.w[d][n] = *(const i32x4_u1*)p;
-                } else {
+        for (int i = 0; i < XI; ++i) {
+            const int r = w + 8 * i;
+            if (512 * p + 512 > a.K) x.r[i].template place<true>(k, a.K);
+            i32x4 parts[C::PARTS];
+            pair_up(x.r[i], parts);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t v = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (at + 4 * j + i < bytes) v |= (uint32_t)p[4 * j + i] << (8 * i);
-                        r.w[d][n][j] = (int)v;
-                    }
-                }
-            }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if ((j & (gr.per - 1)) == 0 && 128 * b + 32 * j < a.K) {
-                const int st = 4 * b + j;
-                const int g = gr.shift >= 0 ? st >> gr.shift : st / gr.steps;
-#pragma unroll
-                for (int d = 0; d < D; ++d)
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        r.s[d][n][j] = srow[d][n][g];
-                        if (zeros) r.z[d][n][j] = zrow[d][n][g];
-                    }
-            }
+            for (int e = 0; e < C::PARTS; ++e) st[e * UNITS + lane * ROWS + (r ^ (lane & 15))] = parts[e];
+        }
+    };
+    auto store_scales = [&](int p, const Ahead& r) {
+        sc[p & 1][0][sr][ss] = (float)r.s;
+        sc[p & 1][1][sr][ss] = 16.0f + (zeros ? (float)r.z : 8.0f);
     };
 
-    float sc[D][NB], zc[D][NB];   // the running group's scale and 16 + zero point
-    f32x4 acc[D][MB][NB], part[D][MB][NB], sx[MB];
+    const Unpack<T> unpack;
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+    const i32x4 ones = {(int)C::ONES, (int)C::ONES, (int)C::ONES, (int)C::ONES};
+    f32x4 acc[MB];
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) acc[d][i][n] = none;
+    for (int i = 0; i < MB; ++i) acc[i] = none;
 
-    auto compute = [&](int b, Blk& r) {
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) transpose4(r.w[d][n]);
-        const i32x4 ones = {(int)C::ONES, (int)C::ONES, (int)C::ONES, (int)C::ONES};
+    auto compute = [&](int p, const Ahead& r) {
+        const int k0 = 512 * p + 128 * run;
+        if (k0 >= a.K) return;
+        i32x4 d = r.w;
+        if (k0 + 128 > a.K && bytes >= 16) d = place_w32(d, (k0 >> 1) + 16 * (lane & 3), bytes);
+        // Rows to operand order: unit (row, chunk) at chunk ^ (row / 2 % 4) of
+        // its row, so that both accesses spread over all banks. A wave's
+        // own units only: no barrier.
+        const int wl = lane >> 2;
+        ws[w][wl * 4 + ((lane & 3) ^ ((wl >> 1) & 3))] = d;
+        d = ws[w][c * 4 + (q ^ ((c >> 1) & 3))];
+        transpose4(d);
+        const i32x4* st = xs[p & 1];
+        f32x4 part[MB], sx[MB];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int k = 128 * b + 32 * j;
-            if (k >= a.K) break;
-            XRaw<T> x[MB];
-#pragma unroll
-            for (int i = 0; i < MB; ++i) x[i].load(xrow[i] + k + 8 * q, a.K - k - 8 * q);
-            const bool first = (j & (gr.per - 1)) == 0;
-            if (first) {
-#pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    sx[i] = none;
-#pragma unroll
-                    for (int d = 0; d < D; ++d)
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) part[d][i][n] = none;
-                }
-#pragma unroll
-                for (int d = 0; d < D; ++d)
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        sc[d][n] = (float)r.s[d][n][j];
-                        zc[d][n] = 16.0f + (zeros ? (float)r.z[d][n][j] : 8.0f);
-                    }
-            }
-            i32x4 u[D][NB];
-#pragma unroll
-            for (int d = 0; d < D; ++d)
-#pragma unroll
-                for (int n = 0; n < NB; ++n) u[d][n] = unpack<T>((uint32_t)r.w[d][n][j]);
+            if (k0 + 32 * j >= a.K) break;
+            const i32x4 u = unpack((uint32_t)d[j]);
+            const int k8 = 16 * run + 4 * j + q;
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
-                i32x4 p[C::PARTS];
-                pair_up(x[i], p);
+                if (j % PER == 0) part[i] = sx[i] = none;
 #pragma unroll
                 for (int e = 0; e < C::PARTS; ++e) {
-                    sx[i] = C::mma(p[e], ones, sx[i]);
-#pragma unroll
-                    for (int d = 0; d < D; ++d)
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) part[d][i][n] = C::mma(p[e], u[d][n], part[d][i][n]);
+                    const i32x4 x = st[e * UNITS + k8 * ROWS + ((16 * i + c) ^ (k8 & 15))];
+                    part[i] = C::mma(x, u, part[i]);
+                    sx[i] = C::mma(x, ones, sx[i]);
                 }
             }
-            const bool last = ((j + 1) & (gr.per - 1)) == 0 || k + 32 >= a.K;
-            if (last) {
+            if ((j + 1) % PER == 0 || k0 + 32 * (j + 1) >= a.K) {
+                const int at = 4 * run + j / PER * PER;
+                const float s = sc[p & 1][0][16 * stream + c][at], z = sc[p & 1][1][16 * stream + c][at];
 #pragma unroll
-                for (int d = 0; d < D; ++d)
+                for (int i = 0; i < MB; ++i)
 #pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        const float s = sc[d][n], z = zc[d][n];
-#pragma unroll
-                        for (int i = 0; i < MB; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[d][i][n][e] =
-                                    __builtin_fmaf(s, __builtin_fmaf(-z, sx[i][e], part[d][i][n][e]), acc[d][i][n][e]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][e] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[i][e], part[i][e]), acc[i][e]);
             }
         }
     };
 
-    // This wave's blocks, two in flight: each next block's loads go out before
-    // the current one's products.
-    if (w < nblk) {
-        Blk r0, r1;
-        load(w, r0);
-        for (int b = w; b < nblk; b += 2 * NW) {
-            if (b + NW < nblk) load(b + NW, r1);
-            __builtin_amdgcn_sched_barrier(0);
-            compute(b, r0);
-            __builtin_amdgcn_sched_barrier(0);
-            if (b + 2 * NW < nblk) load(b + 2 * NW, r0);
-            __builtin_amdgcn_sched_barrier(0);
-            if (b + NW < nblk) compute(b + NW, r1);
-            __builtin_amdgcn_sched_barrier(0);
+    if (passes > 0) {
+        // Each register set is refilled as soon as it is used, so weights are
+        // two passes ahead and X nearly two; the barrier waits for LDS only.
+        Ahead r0, r1;
+        XPass x0, x1;
+        load_x(0, x0);
+        load_ahead(0, r0);
+        load_x(1, x1);
+        load_ahead(1, r1);
+        store_x(0, x0);
+        store_scales(0, r0);
+        load_x(2, x0);
+        ring_barrier<63>();
+        auto pass = [&](int p, Ahead& now, const Ahead& next, XPass& x) {
+            compute(p, now);
+            load_ahead(p + 2, now);
+            store_x(p + 1, x);
+            store_scales(p + 1, next);
+            load_x(p + 3, x);
+            ring_barrier<63>();
+        };
+        for (int p = 0; p < passes; p += 2) {
+            pass(p, r0, r1, x1);
+            if (p + 1 < passes) pass(p + 1, r1, r0, x0);
         }
     }
 
-    // Sums over the waves in their order, one block of 16 features at a time.
+    // Sums over the runs in their order, through the space of X.
+    float* red = (float*)xs;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        if (n > 0) __syncthreads();
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int d = 0; d < D; ++d)
+        for (int e = 0; e < 4; ++e) red[((w * MB + i) * 4 + e) * 68 + lane] = acc[i][e];
+    __syncthreads();
+    for (int o = t; o < MB * 256 * (DUAL ? 1 : 2); o += 512) {
+        const int i = (o >> 4) / (DUAL ? 16 : 32), f = DUAL ? o & 15 : o & 31, row = (o / (DUAL ? 16 : 32)) & 15;
+        float v[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < MB; ++i)
+        for (int d = 0; d < (DUAL ? 2 : 1); ++d)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) red[w][d][i][e][lane] = acc[d][i][n][e];
-        __syncthreads();
-        for (int o = threadIdx.x; o < MB * 256; o += NW * 64) {
-            const int i = o >> 8, row = (o >> 4) & 15, col = o & 15;
-            float v[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int d = 0; d < D; ++d)
-#pragma unroll
-                for (int ww = 0; ww < NW; ++ww) v[d] += red[ww][d][i][row & 3][(row >> 2) * 16 + col];
-            const int m = m0 + 16 * i + row, f = f0 + 16 * n + col;
-            if (m < a.M && f < a.F)
-                ((T*)a.Y)[(int64_t)m * a.ldy + f] = (T)(DUAL ? act_value(a.act, v[0]) * v[1] : v[0]);
-        }
+            for (int rn = 0; rn < 4; ++rn) {
+                const int ww = 2 * rn + (DUAL ? d : f >> 4);
+                v[d] += red[((ww * MB + i) * 4 + (row & 3)) * 68 + (row >> 2) * 16 + (f & 15)];
+            }
+        const int m = m0 + 16 * i + row;
+        if (m < a.M && f0 + f < a.F)
+            ((T*)a.Y)[(int64_t)m * a.ldy + f0 + f] = (T)(DUAL ? act_value(a.act, v[0]) * v[1] : v[0]);
     }
 }
 
 int check_w4(const W4Args& a, bool) {
-    return cdiv(a.M, 16) <= 65535 && cdiv(a.F, 16) <= max_workgroups(1024) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
+    return cdiv(a.M, 16) <= 65535 && cdiv(a.F, 4) <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
-template <class T, bool DUAL, int MB, int NB, int NW>
-static hipError_t launch(const W4Args& a, const W4Groups& gr, hipStream_t s) {
-    const dim3 grid((unsigned)cdiv(a.F, 16 * NB), (unsigned)cdiv(a.M, 16 * MB));
-    hipLaunchKernelGGL((k_w4<T, DUAL, MB, NB, NW>), grid, dim3(NW * 64), 0, s, a, gr);
+template <class T, bool DUAL, int MB, int PER>
+static hipError_t launch_rows(const W4Args& a, const W4Groups& gr, hipStream_t s) {
+    const dim3 grid((unsigned)cdiv(a.F, DUAL ? 16 : 32), (unsigned)cdiv(a.M, 16 * MB));
+    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER>), grid, dim3(512), 0, s, a, gr);
     return hipGetLastError();
 }
 
+template <class T, bool DUAL, int PER>
+static hipError_t launch_any(const W4Args& a, const W4Groups& gr, hipStream_t s) {
+    // Up to two rows the vector units keep up with the weights (8192 x 8192, one
+    // row 10.5 us against 21 on the matrix cores, two 13.4 against 21; four
+    // would be level). They need rows of at least 16 bytes.
+    if (a.M <= 2 && a.K >= 32)
+        return a.M <= 1 ? launch_few<T, DUAL, 1>(a, gr, s) : launch_few<T, DUAL, 2>(a, gr, s);
+    if constexpr (sizeof(T) == 2) {   // (FP32's three parts leave LDS for 16 rows)
+        if (a.M > 32) return launch_rows<T, DUAL, 4, PER>(a, gr, s);
+        if (a.M > 16) return launch_rows<T, DUAL, 2, PER>(a, gr, s);
+    }
+    return launch_rows<T, DUAL, 1, PER>(a, gr, s);
+}
+
 hipError_t launch_w4(int dtype, const W4Args& a, bool dual, hipStream_t s) {
-    W4Groups gr = {a.group / 32, -1, 1};
+    W4Groups gr = {a.group / 32, -1};
     if ((gr.steps & (gr.steps - 1)) == 0) gr.shift = __builtin_ctz(gr.steps);
-    gr.per = gr.steps % 4 == 0 ? 4 : gr.steps % 2 == 0 ? 2 : 1;
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        if (a.M <= 16) {
-            if (dual) return launch<T, true, 1, 1, 8>(a, gr, s);
-            return launch<T, false, 1, 1, 8>(a, gr, s);
-        }
-        if (dual) return launch<T, true, 4, 1, 8>(a, gr, s);
-        return launch<T, false, 4, 2, 8>(a, gr, s);
+        auto go = [&](auto d) {
+            constexpr bool D = decltype(d)::value;
+            if (gr.steps % 4 == 0) return launch_any<T, D, 4>(a, gr, s);
+            if (gr.steps % 2 == 0) return launch_any<T, D, 2>(a, gr, s);
+            return launch_any<T, D, 1>(a, gr, s);
+        };
+        return dual ? go(std::true_type{}) : go(std::false_type{});
     });
 }
 
