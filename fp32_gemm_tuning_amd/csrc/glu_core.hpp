@@ -18,6 +18,7 @@
 #pragma once
 
 #include "ffn.hpp"
+#include "mfma_pipecore.hpp"   // ring_barrier
 
 namespace sgemm {
 
@@ -242,6 +243,189 @@ struct TileCore {
                 for (int r = 0; r < 16; ++r)
                     f(bi, bj, r, wm + 32 * bi + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3),
                       wn + 32 * bj + (lane & 31));
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The same tile filled by buffer-to-LDS loads and software-pipelined, for
+// operands whose lines are whole 16-byte chunks.
+//
+// One workgroup per compute unit: two LDS stages of (BM + BN) x 128 bytes. A
+// slice is four parts; each part's matrix instructions run while the fragments of
+// the next part are read into the other register set. The barrier sits before the
+// last part: every wave has then read the whole stage and its own loads of
+// the next slice have landed, so after it the stage is refilled (the slice
+// after next) and the next slice's first fragments are read, both under the last
+// part's matrix instructions.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kRange = 0x80000000u;   // byte offsets of an operand's tile stay below
+
+// Buffer-to-LDS fill of one operand's part of a slice.
+template <class T, int ROWS, int NT, bool RC>
+struct DmaFill {
+    static constexpr int EPC = Elem<T>::EPC, SLICE = Elem<T>::SLICE;
+    static constexpr int W = NT / 64, PIECES = ROWS / 8;   // of 64 chunks
+    static_assert(PIECES % W == 0, "whole pieces per wave");
+    static constexpr int G = PIECES / W;                   // loads per wave
+    static constexpr int CPL = ROWS / EPC;
+    uint32_t off[G];   // byte offset from the tile's first line, OOB where the line does not exist
+    int q[G];          // KC: first k of the chunk
+
+    // PAIR: which of the two matrices piece p of wave w (8 rows) belongs to.
+    static_assert(W == 4 || W % 8 == 0, "a piece's matrix depends on the wave or on p alone");
+    __device__ __forceinline__ static int matrix(int w, int p) { return W == 4 ? p & 1 : (w >> 2) & 1; }
+
+    // A KC tile's rows start at line r0 (PAIR: of both matrices, as in
+    // RegFill), an RC tile's chunks at element r0 of each line.
+    template <bool PAIR>
+    __device__ __forceinline__ void init(const Lines<T>* s, int r0, int t) {
+        const int w = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
+        const int lines = s[0].lines, extent = s[0].extent;
+#pragma unroll
+        for (int p = 0; p < G; ++p) {
+            const int slot = (w + W * p) * 64 + lane;
+            const int64_t ld = PAIR && matrix(w, p) ? s[1].ld : s[0].ld;
+            if constexpr (RC) {
+                const int k = slot / CPL, c = rc_chunk<ROWS>(k, slot % CPL);
+                off[p] = r0 + c * EPC < extent ? (uint32_t)((k * (int)ld + c * EPC) * (int)sizeof(T)) : OOB;
+            } else {
+                const int row = slot / 8, src = PAIR ? (row >> 6) * 32 + (row & 31) : row;
+                q[p] = ((slot % 8) ^ swz_chunk<32>(row)) * EPC;
+                off[p] = r0 + src < lines ? (uint32_t)((src * (int)ld + q[p]) * (int)sizeof(T)) : OOB;
+            }
+        }
+    }
+    // The slice at k0 of s, whose tile starts at row r0. Past the last k
+    // everything reads as zero.
+    template <bool PAIR>
+    __device__ __forceinline__ void issue(const Lines<T>* both, int r0, int k0, int t, char* lds) const {
+        const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+        const Lines<T>& s = both[0];
+        const int left = (RC ? s.lines : s.extent) - k0;
+        const int kk = __builtin_amdgcn_readfirstlane(left <= 0 ? 0 : left < SLICE ? left : SLICE);
+        const T* base = RC ? s.p + (int64_t)k0 * s.ld + r0 : s.p + (int64_t)r0 * s.ld + k0;
+        // RC: k lines past the last are past the resource's end. KC: rows
+        // that do not exist have the offset OOB, k past the last is masked below.
+        const uint32_t bytes = kk == 0 ? 0u
+                               : RC ? (uint32_t)(((int64_t)(kk - 1) * s.ld + (s.extent - r0)) * (int64_t)sizeof(T))
+                                    : kRange;
+        const __amdgpu_buffer_rsrc_t r = make_rsrc((const float*)base, bytes);
+        __amdgpu_buffer_rsrc_t r1 = r;
+        if constexpr (PAIR) r1 = make_rsrc((const float*)(both[1].p + (int64_t)r0 * both[1].ld + k0), bytes);
+        const bool mask = !RC && kk < SLICE;
+#pragma unroll
+        for (int p = 0; p < G; ++p) {
+            const uint32_t o = mask && q[p] >= kk ? OOB : off[p];
+            if (PAIR && matrix(w, p))
+                buf_load_lds16(r1, (const float*)(lds + (w + W * p) * 1024), o);
+            else
+                buf_load_lds16(r, (const float*)(lds + (w + W * p) * 1024), o);
+        }
+    }
+};
+
+template <class T, int BM, int BN, int WM, int WN, bool ARC, bool BRC, bool PAIR>
+struct DmaCore {
+    static constexpr int WAVES_N = BN / WN;
+    static constexpr int NT = (BM / WM) * WAVES_N * 64;
+    static constexpr int BI = WM / 32, BJ = WN / 32;
+    static constexpr int LDS_A = BM * 128, LDS_B = BN * 128;
+    using FA = DmaFill<T, BM, NT, ARC>;
+    using FB = DmaFill<T, BN, NT, BRC>;
+    using Out = TileCore<T, BM, BN, WM, WN, ARC, BRC, PAIR>;   // for each()
+
+    struct Frag {
+        i32x4 a[BI], b[BJ];
+    };
+
+    // Order of one region's instructions: MFMAS matrix instructions, the reads
+    // of the next part early among them and the fill's loads behind those.
+    template <int LOADS>
+    __device__ __forceinline__ static void weave() {
+        constexpr int MFMA = 0x008, VMEM_READ = 0x020, DS_READ = 0x100;
+        constexpr int MFMAS = BI * BJ * (sizeof(T) == 4 ? 4 : 1);
+        constexpr int READS = BI * (ARC ? 2 : 1) + BJ * (BRC ? 2 : 1);
+        constexpr int RS = (READS + MFMAS - 3) / (MFMAS - 2);   // reads after each of the first ones
+        constexpr int LS = LOADS == 0 ? 1 : (LOADS + MFMAS - 2) / (MFMAS - 1);
+#pragma unroll
+        for (int i = 0; i < MFMAS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+            if (i * RS < READS) __builtin_amdgcn_sched_group_barrier(DS_READ, RS, 0);
+            if (i * LS < LOADS) __builtin_amdgcn_sched_group_barrier(VMEM_READ, LS, 0);
+        }
+    }
+
+    // src(s, A, B[2]) -> first k of slice s, with the operands' lines.
+    template <class Src>
+    __device__ __forceinline__ static void run(char* a0, char* b0, char* a1, char* b1, int m0, int n0,
+                                               int nslices, Src&& src, f32x16 (&acc)[BI][BJ]) {
+        const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+        const int wm = (w / WAVES_N) * WM, wn = (w % WAVES_N) * WN;
+#pragma unroll
+        for (int i = 0; i < BI; ++i)
+#pragma unroll
+            for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        if (nslices <= 0) return;
+        FA fa;
+        FB fb;
+        {
+            Lines<T> la, lb[2];
+            src(0, la, lb);
+            fa.template init<false>(&la, m0, t);
+            fb.template init<PAIR>(lb, n0, t);
+        }
+        auto issue = [&](int s, char* A, char* B) {
+            Lines<T> la, lb[2];
+            const int k0 = src(s, la, lb);
+            fa.template issue<false>(&la, m0, k0, t, A);
+            fb.template issue<PAIR>(lb, n0, k0, t, B);
+        };
+        auto read = [&](Frag& f, const char* A, const char* B, int v) {
+#pragma unroll
+            for (int i = 0; i < BI; ++i) f.a[i] = read_frag<T, BM, ARC>(A, wm + 32 * i, lane, v);
+#pragma unroll
+            for (int j = 0; j < BJ; ++j) f.b[j] = read_frag<T, BN, BRC>(B, wn + 32 * j, lane, v);
+        };
+        auto mma = [&](const Frag& f) {
+#pragma unroll
+            for (int i = 0; i < BI; ++i)
+#pragma unroll
+                for (int j = 0; j < BJ; ++j) mma_chunk(T{}, f.a[i], f.b[j], acc[i][j]);
+        };
+        Frag f0, f1;
+        issue(0, a0, b0);
+        issue(1, a1, b1);   // past the last slice: zeros, never used
+        ring_barrier<FA::G + FB::G>();
+        read(f0, a0, b0, 0);
+        auto slice = [&](int s, char* A, char* B, char* An, char* Bn) {
+            read(f1, A, B, 1);
+            mma(f0);
+            weave<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            read(f0, A, B, 2);
+            mma(f1);
+            weave<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            read(f1, A, B, 3);
+            mma(f0);
+            weave<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            ring_barrier<0>();
+            read(f0, An, Bn, 0);
+            mma(f1);
+            issue(s + 2, A, B);
+            weave<FA::G + FB::G>();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int s = 0;
+        for (; s + 2 <= nslices; s += 2) {
+            slice(s, a0, b0, a1, b1);
+            slice(s + 1, a1, b1, a0, b0);
+        }
+        if (s < nslices) slice(s, a0, b0, a1, b1);
+        ring_barrier<0>();   // the loads past the last slice land before LDS is given up
     }
 };
 

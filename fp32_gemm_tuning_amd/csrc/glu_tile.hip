@@ -6,22 +6,44 @@
 
 namespace sgemm {
 
-static inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 constexpr int GLU_GROUP_M = 8;
+
+// A core's product in LDS of its own: two stages for each operand, as objects
+// apart so that the compiler can tell the stage being filled from the one
+// being read.
+template <class Core, bool DMA, class Src>
+__device__ __forceinline__ void product(int m0, int n0, int nslices, Src&& src,
+                                        f32x16 (&acc)[Core::BI][Core::BJ]) {
+    if constexpr (DMA) {
+        __shared__ __attribute__((aligned(16))) char a0[Core::LDS_A], b0[Core::LDS_B], a1[Core::LDS_A],
+            b1[Core::LDS_B];
+        Core::run(a0, b0, a1, b1, m0, n0, nslices, src, acc);
+    } else {
+        __shared__ __attribute__((aligned(16))) char lds[2 * Core::STAGE];
+        Core::run(lds, m0, n0, nslices, src, acc);
+    }
+}
+
+// Block and wave tile, and how it is filled.
+template <int BM_, int BN_, int WM_, int WN_, bool DMA_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NT = (BM / WM) * (BN / WN) * 64;
+    static constexpr bool DMA = DMA_;
+    template <class T, bool ARC, bool BRC, bool PAIR>
+    using Core = std::conditional_t<DMA_, DmaCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR>,
+                                    TileCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR>>;
+};
 
 // H = act(X Wg^T) * (X Wu^T). A tile's columns alternate between the two
 // weights in blocks of 32, so a wave holds G and U of the same outputs in
 // registers, and neither is written unless the backward pass wants them.
-template <class T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_glu_fwd(GluArgs a, int tiles_m,
-                                                                       int tiles_n, int xcd) {
-    using Core = TileCore<T, BM, BN, WM, WN, false, false, true>;
+template <class T, class Tl>
+__global__ __launch_bounds__(Tl::NT) void k_glu_fwd(GluArgs a, int tiles_m, int tiles_n, int xcd) {
+    using Core = typename Tl::template Core<T, false, false, true>;
     static_assert(Core::BJ % 2 == 0, "a wave holds whole pairs of column blocks");
-    __shared__ __attribute__((aligned(16))) char lds[2 * Core::STAGE];
     int tm, tn;
     tile_of(blockIdx.x, tiles_m, tiles_n, GLU_GROUP_M, xcd != 0, tm, tn);
-    const int m0 = tm * BM, f0 = tn * (BN / 2);
+    const int m0 = __builtin_amdgcn_readfirstlane(tm * Tl::BM), f0 = __builtin_amdgcn_readfirstlane(tn * (Tl::BN / 2));
     f32x16 acc[Core::BI][Core::BJ];
     auto src = [&](int s, Lines<T>& la, Lines<T>* lb) {
         la = Lines<T>{(const T*)a.X, a.ldx, a.M, a.K};
@@ -29,8 +51,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_glu_fwd(GluArgs 
         lb[1] = Lines<T>{(const T*)a.Wu, a.ldwu, a.F, a.K};
         return s * Elem<T>::SLICE;
     };
-    Core::run(lds, m0, f0, (a.K + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
-    Core::each([&](int bi, int bj, int r, int i, int j) {
+    product<Core, Tl::DMA>(m0, f0, (a.K + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
+    TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, false, false, true>::each([&](int bi, int bj, int r, int i, int j) {
         if (bj & 1) return;
         const int row = m0 + i, f = f0 + (j >> 6) * 32 + (j & 31);
         if (row >= a.M || f >= a.F) return;
@@ -45,73 +67,95 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_glu_fwd(GluArgs 
 
 // dX = dG Wg + dU Wu as one sum over 2F: first the slices of dG and Wg, then
 // those of dU and Wu.
-template <class T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_glu_dx(GluProdArgs a, int tiles_m,
-                                                                      int tiles_n, int xcd) {
-    using Core = TileCore<T, BM, BN, WM, WN, false, true, false>;
-    __shared__ __attribute__((aligned(16))) char lds[2 * Core::STAGE];
+template <class T, class Tl>
+__global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, int tiles_n, int xcd) {
+    using Core = typename Tl::template Core<T, false, true, false>;
     int tm, tn;
     tile_of(blockIdx.x, tiles_m, tiles_n, GLU_GROUP_M, xcd != 0, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
+    const int m0 = __builtin_amdgcn_readfirstlane(tm * Tl::BM), n0 = __builtin_amdgcn_readfirstlane(tn * Tl::BN);
     const int half = (a.F + Elem<T>::SLICE - 1) / Elem<T>::SLICE;
     f32x16 acc[Core::BI][Core::BJ];
     auto src = [&](int s, Lines<T>& la, Lines<T>* lb) {
         const int u = s >= half;
-        la = Lines<T>{(const T*)a.D[u], a.ldd, a.M, a.F};
-        lb[0] = Lines<T>{(const T*)a.W[u], a.ldw[u], a.F, a.K};
+        // (dG and dU are zero from F to whole slices)
+        la = Lines<T>{(const T*)(u ? a.D[1] : a.D[0]), a.ldd, a.M, half * Elem<T>::SLICE};
+        lb[0] = Lines<T>{(const T*)(u ? a.W[1] : a.W[0]), a.ldw[0], a.F, a.K};
+        if (!Tl::DMA) lb[0].ld = u ? a.ldw[1] : a.ldw[0];
         return (s - u * half) * Elem<T>::SLICE;
     };
-    Core::run(lds, m0, n0, 2 * half, src, acc);
-    Core::each([&](int bi, int bj, int r, int i, int j) {
+    product<Core, Tl::DMA>(m0, n0, 2 * half, src, acc);
+    TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, false, true, false>::each([&](int bi, int bj, int r, int i, int j) {
         const int row = m0 + i, col = n0 + j;
         if (row < a.M && col < a.K) ((T*)a.C[0])[(int64_t)row * a.ldc[0] + col] = (T)acc[bi][bj][r];
     });
 }
 
 // dWg = dG^T X (blockIdx.y 0) and dWu = dU^T X (1): sums over the M tokens.
-template <class T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_glu_dw(GluProdArgs a, int tiles_m,
-                                                                      int tiles_n, int xcd) {
-    using Core = TileCore<T, BM, BN, WM, WN, true, true, false>;
-    __shared__ __attribute__((aligned(16))) char lds[2 * Core::STAGE];
+template <class T, class Tl>
+__global__ __launch_bounds__(Tl::NT) void k_glu_dw(GluProdArgs a, int tiles_m, int tiles_n, int xcd) {
+    using Core = typename Tl::template Core<T, true, true, false>;
     const int u = a.C[0] == nullptr ? 1 : blockIdx.y;
     int tm, tn;
     tile_of(blockIdx.x, tiles_m, tiles_n, GLU_GROUP_M, xcd != 0, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
+    const int m0 = __builtin_amdgcn_readfirstlane(tm * Tl::BM), n0 = __builtin_amdgcn_readfirstlane(tn * Tl::BN);
     f32x16 acc[Core::BI][Core::BJ];
     auto src = [&](int s, Lines<T>& la, Lines<T>* lb) {
-        la = Lines<T>{(const T*)a.D[u], a.ldd, a.M, a.F};
+        la = Lines<T>{(const T*)(u ? a.D[1] : a.D[0]), a.ldd, a.M, (a.F + 63) / 64 * 64};
         lb[0] = Lines<T>{(const T*)a.X, a.ldx, a.M, a.K};
         return s * Elem<T>::SLICE;
     };
-    Core::run(lds, m0, n0, (a.M + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
-    Core::each([&](int bi, int bj, int r, int i, int j) {
+    product<Core, Tl::DMA>(m0, n0, (a.M + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
+    TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, true, true, false>::each([&](int bi, int bj, int r, int i, int j) {
         const int f = m0 + i, col = n0 + j;
-        if (f < a.F && col < a.K) ((T*)a.C[u])[(int64_t)f * a.ldc[u] + col] = (T)acc[bi][bj][r];
+        T* const C = (T*)(u ? a.C[1] : a.C[0]);
+        if (f < a.F && col < a.K) C[(int64_t)f * (u ? a.ldc[1] : a.ldc[0]) + col] = (T)acc[bi][bj][r];
     });
 }
 
-constexpr int GB = 128, GW = 64;   // block and wave tile
-constexpr int GNT = (GB / GW) * (GB / GW) * 64;
+using TileReg = Tile<128, 128, 64, 64, false>;
+using TileMid = Tile<128, 128, 64, 64, true>;
+using TileBig = Tile<256, 256, 128, 64, true>;
+
+// Whether an operand of `lines` lines can be filled by buffer-to-LDS loads:
+// whole 16-byte chunks, and a tile's span within 31-bit byte offsets.
+static bool dma_ok(int dtype, const void* p, int64_t ld, int64_t extent, int64_t tile_lines) {
+    const int64_t e = dtype_bytes(dtype), chunk = 16 / e;
+    return aligned16(p) && ld % chunk == 0 && extent % chunk == 0 &&
+           ((tile_lines - 1) * ld + extent) * e < (int64_t)kRange;
+}
+
+// f(tile tag): the register-filled tile where an operand is not whole
+// chunks, else the big tile where it gives every compute unit work.
+template <class Fn>
+static hipError_t with_tile(bool dma, int64_t rows, int64_t cols, int64_t copies, Fn&& f) {
+    if (!dma) return f(TypeTag<TileReg>{});
+    if (cdiv(rows, 256) * cdiv(cols, 256) * copies >= 192) return f(TypeTag<TileBig>{});
+    return f(TypeTag<TileMid>{});
+}
 
 int check_glu(const GluArgs& a) {
-    const int64_t tiles = cdiv(a.M, GB) * cdiv(a.F, GB / 2);
-    return tiles <= max_workgroups(GNT) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
+    const int64_t tiles = cdiv(a.M, 128) * cdiv(a.F, 64);
+    return tiles <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
 hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s) {
-    const int tm = (int)cdiv(a.M, GB), tn = (int)cdiv(a.F, GB / 2);
+    const bool dma = dma_ok(dtype, a.X, a.ldx, a.K, 256) && dma_ok(dtype, a.Wg, a.ldwg, a.K, 128) &&
+                     dma_ok(dtype, a.Wu, a.ldwu, a.K, 128);
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        hipLaunchKernelGGL((k_glu_fwd<T, GB, GB, GW, GW>), dim3((unsigned)((int64_t)tm * tn)), dim3(GNT),
-                           0, s, a, tm, tn, xcd_remap_enabled());
-        return hipGetLastError();
+        return with_tile(dma, a.M, 2 * (int64_t)a.F, 1, [&](auto tile) {
+            using Tl = typename decltype(tile)::type;
+            const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.F, Tl::BN / 2);
+            hipLaunchKernelGGL((k_glu_fwd<T, Tl>), dim3((unsigned)((int64_t)tm * tn)), dim3(Tl::NT), 0, s, a, tm,
+                               tn, xcd_remap_enabled());
+            return hipGetLastError();
+        });
     });
 }
 
 int check_glu_prod(const GluProdArgs& a) {
-    const int64_t x = cdiv(a.M, GB) * cdiv(a.K, GB), w = cdiv(a.F, GB) * cdiv(a.K, GB);
-    return x <= max_workgroups(GNT) && w <= max_workgroups(GNT) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
+    const int64_t x = cdiv(a.M, 128) * cdiv(a.K, 128), w = cdiv(a.F, 128) * cdiv(a.K, 128);
+    return x <= max_workgroups(512) && w <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
 template <class Fn>
@@ -121,23 +165,33 @@ static hipError_t with_half(int dtype, Fn&& f) {
 }
 
 hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s) {
-    const int tm = (int)cdiv(a.M, GB), tn = (int)cdiv(a.K, GB);
+    // One tile's lines: 256 rows of dG, or a slice's 64 of W.
+    const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 256) && dma_ok(dtype, a.W[0], a.ldw[0], a.K, 64) &&
+                     dma_ok(dtype, a.W[1], a.ldw[1], a.K, 64) && a.ldw[0] == a.ldw[1];
     return with_half(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        hipLaunchKernelGGL((k_glu_dx<T, GB, GB, GW, GW>), dim3((unsigned)((int64_t)tm * tn)), dim3(GNT),
-                           0, s, a, tm, tn, xcd_remap_enabled());
-        return hipGetLastError();
+        return with_tile(dma, a.M, a.K, 1, [&](auto tile) {
+            using Tl = typename decltype(tile)::type;
+            const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.K, Tl::BN);
+            hipLaunchKernelGGL((k_glu_dx<T, Tl>), dim3((unsigned)((int64_t)tm * tn)), dim3(Tl::NT), 0, s, a, tm,
+                               tn, xcd_remap_enabled());
+            return hipGetLastError();
+        });
     });
 }
 
 hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s) {
-    const int tm = (int)cdiv(a.F, GB), tn = (int)cdiv(a.K, GB);
     const unsigned both = a.C[0] != nullptr && a.C[1] != nullptr ? 2 : 1;
+    const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 64) && dma_ok(dtype, a.X, a.ldx, a.K, 64);
     return with_half(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        hipLaunchKernelGGL((k_glu_dw<T, GB, GB, GW, GW>), dim3((unsigned)((int64_t)tm * tn), both),
-                           dim3(GNT), 0, s, a, tm, tn, xcd_remap_enabled());
-        return hipGetLastError();
+        return with_tile(dma, a.F, a.K, both, [&](auto tile) {
+            using Tl = typename decltype(tile)::type;
+            const int tm = (int)cdiv(a.F, Tl::BM), tn = (int)cdiv(a.K, Tl::BN);
+            hipLaunchKernelGGL((k_glu_dw<T, Tl>), dim3((unsigned)((int64_t)tm * tn), both), dim3(Tl::NT), 0, s, a,
+                               tm, tn, xcd_remap_enabled());
+            return hipGetLastError();
+        });
     });
 }
 

@@ -86,6 +86,30 @@ def test_glu_whole_numbers(dev, shape, dtype, layout):
     assert torch.equal(H2, H)
 
 
+# Enough tiles for the largest block tile in each product (H: M x 2F, dX:
+# M x K, dW: F x K), with ragged edges in whole 16-byte chunks.
+LARGE = [(3000, 4136, 144), (2904, 72, 4200), (72, 2600, 2728), (520, 264, 200)]
+
+
+@pytest.mark.parametrize("dtype", ref.DTYPES)
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_large_whole_numbers(dev, shape, dtype):
+    M, F, K = shape
+    t = ref.DTYPES[dtype]
+    _say("large ints", shape, dtype)
+    gen = _gen(14, shape)
+    X, Wg, Wu, dH = (_ints(s, gen, -1, 1, dev, t) for s in ((M, K), (F, K), (F, K), (M, F)))
+    H, flat = _out(M, F, t, dev, 8, 8)
+    sg.glu(X, Wg, Wu, "relu", out=H)
+    x, wg, wu, dh = (v.double() for v in (X, Wg, Wu, dH))
+    g, u = x @ wg.T, x @ wu.T
+    assert torch.equal(H, (g.clamp(min=0) * u).to(t)) and ref.around_untouched(flat, H)
+    got = _backward(dH, X, Wg, Wu, "relu", (0, 0), dev)
+    dg, du = (dh * u * (g > 0)).to(t).double(), (dh * g.clamp(min=0)).to(t).double()
+    for name, a, b in zip(("dX", "dWg", "dWu"), got, (dg @ wg + du @ wu, dg.T @ x, du.T @ x)):
+        assert torch.equal(a, b.to(t)), name
+
+
 @pytest.mark.parametrize("act", ref.ACTS)
 @pytest.mark.parametrize("dtype", ref.DTYPES)
 @pytest.mark.parametrize("shape", [(1, 64, 256), (9, 130, 77), (200, 150, 300)], ids=str)
