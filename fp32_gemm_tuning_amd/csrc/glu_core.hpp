@@ -72,26 +72,34 @@ struct Lines {
     int lines, extent;
 };
 
-// The chunk of EPC elements of a line from `at`: elements past the extent, and
-// lines that do not exist, are zero. Nothing outside the line is read.
-template <class T>
+// The chunk of EPC elements of a line from `at`, in two steps, so that a tile's
+// loads are all in flight at once (a load in a divergent branch would be
+// waited for there). load_chunk reads EPC elements of the line without a
+// branch: the line's last ones where the chunk would reach past its end, the last
+// line where the line does not exist. place_chunk moves the chunk's elements
+// into place, zeros behind them. Lines shorter than a chunk (SHORT) are read
+// element by element. Nothing outside the lines is read.
+template <bool SHORT, class T>
 __device__ __forceinline__ i32x4 load_chunk(const Lines<T>& s, int line, int at) {
     constexpr int EPC = Elem<T>::EPC;
-    i32x4 v = {0, 0, 0, 0};
-    if (line < s.lines && at < s.extent) {
-        const T* p = s.p + (int64_t)line * s.ld + at;
-        if (at + EPC <= s.extent) {
-            v = *(const i32x4_u2*)p;
-        } else {
-            typedef T Vec __attribute__((ext_vector_type(EPC)));
-            Vec x = __builtin_bit_cast(Vec, v);
+    const T* p = s.p + (int64_t)(line < s.lines ? line : s.lines - 1) * s.ld;
+    if constexpr (!SHORT) return *(const i32x4_u2*)(p + (at < s.extent - EPC ? at : s.extent - EPC));
+    typedef T Vec __attribute__((ext_vector_type(EPC)));
+    Vec x = __builtin_bit_cast(Vec, i32x4{0, 0, 0, 0});
 #pragma unroll
-            for (int e = 0; e < EPC; ++e)
-                if (at + e < s.extent) x[e] = p[e];
-            v = __builtin_bit_cast(i32x4, x);
-        }
+    for (int e = 0; e < EPC; ++e) {
+        const T y = p[at + e < s.extent ? at + e : s.extent - 1];
+        x[e] = at + e < s.extent ? y : (T)0.0f;
     }
-    return v;
+    return __builtin_bit_cast(i32x4, x);
+}
+template <bool SHORT, class T>
+__device__ __forceinline__ i32x4 place_chunk(const i32x4& v, const Lines<T>& s, int line, int at) {
+    constexpr int EPC = Elem<T>::EPC;
+    const int past = SHORT ? 0 : at - (s.extent - EPC);   // elements to drop
+    const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, v);
+    const bool none = line >= s.lines || past >= EPC;
+    return __builtin_bit_cast(i32x4, none ? (unsigned __int128)0 : x >> (past > 0 ? 8 * (int)sizeof(T) * past : 0));
 }
 
 // LDS placement of an RC operand's 16-byte chunk (k line, chunk of 8 rows):
@@ -104,7 +112,7 @@ __device__ __forceinline__ int rc_chunk(int kline, int c) {
 
 // Register-staged fill of one operand's part of a slice: NT threads, CH
 // chunks each.
-template <class T, int ROWS, int NT, bool RC>
+template <class T, int ROWS, int NT, bool RC, bool SHORT>
 struct RegFill {
     static constexpr int EPC = Elem<T>::EPC;
     static constexpr int CHUNKS = ROWS * 8;
@@ -113,29 +121,38 @@ struct RegFill {
     static constexpr int CPL = ROWS / EPC;   // chunks per k line (RC)
     i32x4 v[CH];
 
-    // Slice of k0 .. k0 + SLICE - 1, tile rows from r0. A KC operand may be
-    // two matrices whose rows alternate in blocks of 32 (PAIR: block b of the tile
-    // is block b / 2 of matrix b % 2, both from row r0).
+    // The chunk of slot `slot`: its line and its place along it. Slice of k0 ..
+    // k0 + SLICE - 1, tile rows from r0. A KC operand may be two matrices whose
+    // rows alternate in blocks of 32 (PAIR: block b of the tile is block b / 2
+    // of matrix b % 2, both from row r0).
+    template <bool PAIR>
+    __device__ __forceinline__ static void where(int slot, int r0, int k0, int& line, int& at) {
+        if constexpr (RC) {
+            line = k0 + slot / CPL;
+            at = r0 + (slot % CPL) * EPC;
+        } else {
+            const int row = slot / 8;
+            line = r0 + (PAIR ? (row >> 6) * 32 + (row & 31) : row);
+            at = k0 + (slot % 8) * EPC;
+        }
+    }
     template <bool PAIR>
     __device__ __forceinline__ void load(const Lines<T>* s, int r0, int k0, int t) {
 #pragma unroll
         for (int p = 0; p < CH; ++p) {
             const int slot = t + NT * p;
-            if constexpr (RC) {
-                v[p] = load_chunk(s[0], k0 + slot / CPL, r0 + (slot % CPL) * EPC);
-            } else {
-                const int row = slot / 8, at = k0 + (slot % 8) * EPC;
-                if constexpr (PAIR) {
-                    const bool u = (row >> 5) & 1;
-                    const Lines<T> q = {u ? s[1].p : s[0].p, u ? s[1].ld : s[0].ld, s[0].lines, s[0].extent};
-                    v[p] = load_chunk(q, r0 + (row >> 6) * 32 + (row & 31), at);
-                }
-                else
-                    v[p] = load_chunk(s[0], r0 + row, at);
-            }
+            int line, at;
+            where<PAIR>(slot, r0, k0, line, at);
+            const bool u = PAIR && ((slot / 8 >> 5) & 1);
+            v[p] = load_chunk<SHORT>(Lines<T>{u ? s[1].p : s[0].p, u ? s[1].ld : s[0].ld, s[0].lines, s[0].extent}, line, at);
         }
     }
-    __device__ __forceinline__ void store(char* lds, int t) const {
+    template <bool PAIR>
+    __device__ __forceinline__ void store(char* lds, const Lines<T>* s, int r0, int k0, int t) const {
+        // A slice wholly inside its operand needs no placing.
+        constexpr int SLICE = Elem<T>::SLICE, TR = PAIR ? ROWS / 2 : ROWS;
+        const bool whole = RC ? k0 + SLICE <= s[0].lines && r0 + TR <= s[0].extent
+                              : k0 + SLICE <= s[0].extent && r0 + TR <= s[0].lines;
 #pragma unroll
         for (int p = 0; p < CH; ++p) {
             const int slot = t + NT * p;
@@ -147,7 +164,13 @@ struct RegFill {
                 const int row = slot / 8;
                 at = row * 8 + ((slot % 8) ^ swz_chunk<32>(row));
             }
-            *(i32x4*)(lds + at * 16) = v[p];
+            i32x4 x = v[p];
+            if (!whole) {
+                int line, place;
+                where<PAIR>(slot, r0, k0, line, place);
+                x = place_chunk<SHORT>(x, s[0], line, place);
+            }
+            *(i32x4*)(lds + at * 16) = x;
         }
     }
 };
@@ -173,7 +196,7 @@ __device__ __forceinline__ i32x4 read_frag(const char* lds, int row0, int lane, 
 // The product of one tile: BM x BN outputs, waves of WM x WN, both operands
 // through registers into two LDS stages. `nslices` slices; slice s takes its
 // operands from sources src(s, A sources, B sources) -> first k.
-template <class T, int BM, int BN, int WM, int WN, bool ARC, bool BRC, bool PAIR>
+template <class T, int BM, int BN, int WM, int WN, bool ARC, bool BRC, bool PAIR, bool SHORT = false>
 struct TileCore {
     static constexpr int WAVES_N = BN / WN;
     static constexpr int NT = (BM / WM) * WAVES_N * 64;
@@ -192,18 +215,19 @@ struct TileCore {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
         if (nslices <= 0) return;
-        RegFill<T, BM, NT, ARC> fa;
-        RegFill<T, BN, NT, BRC> fb;
+        RegFill<T, BM, NT, ARC, SHORT> fa;
+        RegFill<T, BN, NT, BRC, SHORT> fb;
+        Lines<T> la, lb[2];   // of the slice in flight
+        int k0 = 0;
         auto load = [&](int s) {
-            Lines<T> la, lb[2];
-            const int k0 = src(s, la, lb);
+            k0 = src(s, la, lb);
             fa.template load<false>(&la, m0, k0, t);
             fb.template load<PAIR>(lb, n0, k0, t);
         };
         auto store = [&](int s) {
             char* st = lds + (s & 1) * STAGE;
-            fa.store(st, t);
-            fb.store(st + BM * 128, t);
+            fa.template store<false>(st, &la, m0, k0, t);
+            fb.template store<PAIR>(st + BM * 128, lb, n0, k0, t);
         };
         load(0);
         store(0);

@@ -24,14 +24,15 @@ __device__ __forceinline__ void product(int m0, int n0, int nslices, Src&& src,
     }
 }
 
-// Block and wave tile, and how it is filled.
-template <int BM_, int BN_, int WM_, int WN_, bool DMA_>
+// Block and wave tile, and how it is filled: buffer-to-LDS loads (DMA) or
+// through registers, element by element where rows are shorter than 16 bytes.
+template <int BM_, int BN_, int WM_, int WN_, bool DMA_, bool SHORT_ = false>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NT = (BM / WM) * (BN / WN) * 64;
     static constexpr bool DMA = DMA_;
     template <class T, bool ARC, bool BRC, bool PAIR>
     using Core = std::conditional_t<DMA_, DmaCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR>,
-                                    TileCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR>>;
+                                    TileCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, SHORT_>>;
 };
 
 // H = act(X Wg^T) * (X Wu^T). A tile's columns alternate between the two
@@ -113,6 +114,7 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dw(GluProdArgs a, int tiles_m, i
 }
 
 using TileReg = Tile<128, 128, 64, 64, false>;
+using TileShort = Tile<128, 128, 64, 64, false, true>;
 using TileMid = Tile<128, 128, 64, 64, true>;
 using TileBig = Tile<256, 256, 128, 64, true>;
 
@@ -127,7 +129,8 @@ static bool dma_ok(int dtype, const void* p, int64_t ld, int64_t extent, int64_t
 // f(tile tag): the register-filled tile where an operand is not whole
 // chunks, else the big tile where it gives every compute unit work.
 template <class Fn>
-static hipError_t with_tile(bool dma, int64_t rows, int64_t cols, int64_t copies, Fn&& f) {
+static hipError_t with_tile(int dtype, int K, bool dma, int64_t rows, int64_t cols, int64_t copies, Fn&& f) {
+    if (K < 16 / dtype_bytes(dtype)) return f(TypeTag<TileShort>{});
     if (!dma) return f(TypeTag<TileReg>{});
     if (cdiv(rows, 256) * cdiv(cols, 256) * copies >= 192) return f(TypeTag<TileBig>{});
     return f(TypeTag<TileMid>{});
@@ -143,7 +146,7 @@ hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s) {
                      dma_ok(dtype, a.Wu, a.ldwu, a.K, 128);
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        return with_tile(dma, a.M, 2 * (int64_t)a.F, 1, [&](auto tile) {
+        return with_tile(dtype, a.K, dma, a.M, 2 * (int64_t)a.F, 1, [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.F, Tl::BN / 2);
             hipLaunchKernelGGL((k_glu_fwd<T, Tl>), dim3((unsigned)((int64_t)tm * tn)), dim3(Tl::NT), 0, s, a, tm,
@@ -170,7 +173,7 @@ hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s) {
                      dma_ok(dtype, a.W[1], a.ldw[1], a.K, 64) && a.ldw[0] == a.ldw[1];
     return with_half(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        return with_tile(dma, a.M, a.K, 1, [&](auto tile) {
+        return with_tile(dtype, a.K, dma, a.M, a.K, 1, [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.K, Tl::BN);
             hipLaunchKernelGGL((k_glu_dx<T, Tl>), dim3((unsigned)((int64_t)tm * tn)), dim3(Tl::NT), 0, s, a, tm,
@@ -185,7 +188,7 @@ hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s) {
     const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 64) && dma_ok(dtype, a.X, a.ldx, a.K, 64);
     return with_half(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        return with_tile(dma, a.F, a.K, both, [&](auto tile) {
+        return with_tile(dtype, a.K, dma, a.F, a.K, both, [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.F, Tl::BM), tn = (int)cdiv(a.K, Tl::BN);
             hipLaunchKernelGGL((k_glu_dw<T, Tl>), dim3((unsigned)((int64_t)tm * tn), both), dim3(Tl::NT), 0, s, a,

@@ -70,40 +70,52 @@ struct Unpack {
 template <class T>
 struct XRaw {
     i32x4 v[sizeof(T) / 2];
-    // Elements at .. at + 7 of a row of n elements; place() zeroes those past
-    // its end. Apart, and without branches, as load_w32.
-    template <bool RAGGED>   // else all 8 exist, or none
+    // Elements at .. at + 7 of a row of n >= 8 elements: fetch reads the last 8
+    // where these would reach past the row's end, and place moves them down, zeros
+    // behind. Apart, and without branches in fetch, so that many loads are in
+    // flight: a value that a branch may set otherwise is waited for there.
     __device__ __forceinline__ void fetch(const T* row, int at, int n) {
-        if constexpr (!RAGGED) {
-            typedef i32x4 V __attribute__((aligned(2)));
-            const T* p = row + (at < n ? at : 0);
+        typedef i32x4 V __attribute__((aligned(2)));
+        const T* p = row + (at < n - 8 ? at : n - 8);
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = ((const V*)p)[i];
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = ((const V*)p)[i];
+    }
+    __device__ __forceinline__ void place(int at, int n) {
+        const int past = at - (n - 8);
+        if constexpr (sizeof(T) == 2) {
+            const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, v[0]);
+            v[0] = __builtin_bit_cast(i32x4, past >= 8 ? (unsigned __int128)0 : x >> (past > 0 ? 16 * past : 0));
         } else {
-            constexpr int EPV = 16 / sizeof(T);
-            typedef T E __attribute__((ext_vector_type(EPV)));
+            const bool by4 = past & 4, by2 = past & 2, by1 = past & 1;
+            int x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+            if (past >= 8) {
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-                E x;
+                for (int e = 0; e < 8; ++e) x[e] = 0;
+            } else if (past > 0) {
 #pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    const int k = at + i * EPV + e;
-                    x[e] = row[k < n ? k : n - 1];
-                }
-                v[i] = __builtin_bit_cast(i32x4, x);
+                for (int e = 0; e < 8; ++e) x[e] = by4 ? (e < 4 ? x[e + 4] : 0) : x[e];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = by2 ? (e < 6 ? x[e + 2] : 0) : x[e];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = by1 ? (e < 7 ? x[e + 1] : 0) : x[e];
             }
+            v[0] = i32x4{x[0], x[1], x[2], x[3]};
+            v[1] = i32x4{x[4], x[5], x[6], x[7]};
         }
     }
-    template <bool RAGGED>
-    __device__ __forceinline__ void place(int at, int n) {
+    // The same of a row of any length, element by element.
+    __device__ __forceinline__ void fetch_short(const T* row, int at, int n) {
         constexpr int EPV = 16 / sizeof(T);
         typedef T E __attribute__((ext_vector_type(EPV)));
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-            E x = __builtin_bit_cast(E, v[i]);
+            E x;
 #pragma unroll
-            for (int e = 0; e < EPV; ++e)
-                if (at + (RAGGED ? i * EPV + e : 0) >= n) x[e] = (T)0.0f;
+            for (int e = 0; e < EPV; ++e) {
+                const int k = at + i * EPV + e;
+                const T y = row[k < n ? k : n - 1];
+                x[e] = k < n ? y : (T)0.0f;
+            }
             v[i] = __builtin_bit_cast(i32x4, x);
         }
     }
@@ -288,7 +300,7 @@ __global__ __launch_bounds__(512) void k_w4_few(W4Args a, W4Groups gr, int kw) {
         for (int m = 0; m < MR; ++m) {
             const T* row = (const T*)a.X + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[m][j].template fetch<RAGGED>(row, k + 8 * j, a.K);
+            for (int j = 0; j < 4; ++j) x[m][j].fetch(row, k + 8 * j, a.K);
         }
         // Row by row, so that the first rows' products run while the last ones'
         // weights arrive. Without zero points the scale is read twice and the
@@ -311,7 +323,7 @@ __global__ __launch_bounds__(512) void k_w4_few(W4Args a, W4Groups gr, int kw) {
 #pragma unroll
         for (int m = 0; m < MR; ++m) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[m][j].template place<RAGGED>(k + 8 * j, a.K);
+            for (int j = 0; j < 4; ++j) x[m][j].place(k + 8 * j, a.K);
             lx[m].set(x[m]);
         }
 #pragma unroll
@@ -388,7 +400,8 @@ __device__ __forceinline__ void transpose4(i32x4& d) {
     d = i32x4{(int)c[0], (int)c[1], (int)e[0], (int)e[1]};
 }
 
-template <class T, bool DUAL, int MB, int PER>
+// SHORT: K < 32, rows too short for whole loads.
+template <class T, bool DUAL, int MB, int PER, bool SHORT = false>
 __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
     using C = W4Type<T>;
     constexpr int ROWS = 16 * MB, UNITS = 64 * ROWS;   // 16-byte units of a part's pass
@@ -423,7 +436,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
     };
     auto load_ahead = [&](int p, Ahead& r) {
         const int at = 256 * p + 64 * run + 16 * (lane & 3);
-        if (bytes >= 16) {
+        if constexpr (!SHORT) {
             r.w = load_w32(wrow, at, bytes);
         } else {
             unsigned __int128 x = 0;
@@ -443,10 +456,10 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
         for (int i = 0; i < XI; ++i) {
             const int m = m0 + w + 8 * i;
             const T* row = (const T*)a.X + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
-            if (a.K % 8 == 0 || 512 * p + 512 <= a.K)
-                x.r[i].template fetch<false>(row, k, a.K);
+            if constexpr (SHORT)
+                x.r[i].fetch_short(row, k, a.K);
             else
-                x.r[i].template fetch<true>(row, k, a.K);
+                x.r[i].fetch(row, k, a.K);
         }
     };
     auto store_x = [&](int p, XPass& x) {
@@ -455,7 +468,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
             const int r = w + 8 * i;
-            if (512 * p + 512 > a.K) x.r[i].template place<true>(k, a.K);
+            if (!SHORT && 512 * p + 512 > a.K) x.r[i].place(k, a.K);
             i32x4 parts[C::PARTS];
             pair_up(x.r[i], parts);
 #pragma unroll
@@ -478,7 +491,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
         const int k0 = 512 * p + 128 * run;
         if (k0 >= a.K) return;
         i32x4 d = r.w;
-        if (k0 + 128 > a.K && bytes >= 16) d = place_w32(d, (k0 >> 1) + 16 * (lane & 3), bytes);
+        if (!SHORT && k0 + 128 > a.K) d = place_w32(d, (k0 >> 1) + 16 * (lane & 3), bytes);
         // Rows to operand order: unit (row, chunk) at chunk ^ (row / 2 % 4) of
         // its row, so that both accesses spread over all banks. A wave's
         // own units only: no barrier.
@@ -569,10 +582,10 @@ int check_w4(const W4Args& a, bool) {
     return cdiv(a.M, 16) <= 65535 && cdiv(a.F, 4) <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
-template <class T, bool DUAL, int MB, int PER>
+template <class T, bool DUAL, int MB, int PER, bool SHORT = false>
 static hipError_t launch_rows(const W4Args& a, const W4Groups& gr, hipStream_t s) {
     const dim3 grid((unsigned)cdiv(a.F, DUAL ? 16 : 32), (unsigned)cdiv(a.M, 16 * MB));
-    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER>), grid, dim3(512), 0, s, a, gr);
+    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER, SHORT>), grid, dim3(512), 0, s, a, gr);
     return hipGetLastError();
 }
 
@@ -580,8 +593,8 @@ template <class T, bool DUAL, int PER>
 static hipError_t launch_any(const W4Args& a, const W4Groups& gr, hipStream_t s) {
     // Up to two rows the vector units keep up with the weights (8192 x 8192, one
     // row 10.5 us against 21 on the matrix cores, two 13.4 against 21; four
-    // would be level). They need rows of at least 16 bytes.
-    if (a.M <= 2 && a.K >= 32)
+    // would be level).
+    if (a.M <= 2)
         return a.M <= 1 ? launch_few<T, DUAL, 1>(a, gr, s) : launch_few<T, DUAL, 2>(a, gr, s);
     if constexpr (sizeof(T) == 2) {   // (FP32's three parts leave LDS for 16 rows)
         if (a.M > 32) return launch_rows<T, DUAL, 4, PER>(a, gr, s);
@@ -597,6 +610,7 @@ hipError_t launch_w4(int dtype, const W4Args& a, bool dual, hipStream_t s) {
         using T = typename decltype(tag)::type;
         auto go = [&](auto d) {
             constexpr bool D = decltype(d)::value;
+            if (a.K < 32) return launch_rows<T, D, 1, 1, true>(a, gr, s);
             if (gr.steps % 4 == 0) return launch_any<T, D, 4>(a, gr, s);
             if (gr.steps % 2 == 0) return launch_any<T, D, 2>(a, gr, s);
             return launch_any<T, D, 1>(a, gr, s);

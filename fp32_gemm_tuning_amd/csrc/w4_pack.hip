@@ -6,14 +6,18 @@ namespace sgemm {
 
 static inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The stored number of w: quotient, rounding and offset in 64 bits. The
-// operands have at most 24 significant bits and the quotient is compared with
-// halves of small whole numbers, so the 64-bit quotient never rounds across a
-// half that the exact one does not reach.
-__device__ __forceinline__ uint32_t quantise(float w, double s, double z) {
-    double q = (s != 0.0 ? rint((double)w / s) : 0.0) + z;
-    q = q < 0.0 ? 0.0 : q > 15.0 ? 15.0 : q;
-    return q == q ? (uint32_t)(int)q : (uint32_t)(int)z;
+// The stored number of w, from the exact quotient w / s rounded to even: the
+// FP32 product with 1 / s is within 2^-19 of the quotient (at most 16 in
+// magnitude, each of three roundings 2^-24 of it), so unless it lies that close
+// to a half its nearest whole number is the quotient's. Closer ones take the
+// 64-bit quotient: operands of 24 bits against halves of small whole numbers,
+// which it never rounds across.
+__device__ __forceinline__ uint32_t quantise(float w, float s, float inv, float z) {
+    const float x = w * inv;
+    float n = rintf(x);
+    if (fabsf(x - n) > 0.49999f) n = (float)rint((double)w / (double)s);
+    n = fminf(fmaxf(n + z, 0.0f), 15.0f);
+    return (uint32_t)(int)n;
 }
 
 // One wave per group of one row.
@@ -43,21 +47,32 @@ __global__ __launch_bounds__(256) void k_w4_quantize(PackArgs a) {
     const bool asym = a.Z != nullptr;
     const double exact = asym ? ((double)hi - (double)lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
     const T st = bad == 0.0f ? (T)(float)exact : (T)__builtin_nanf("");
-    const double s = (double)(float)st;
-    double z = 8.0;
-    if (asym) {
-        z = s > 0.0 ? rint(-(double)lo / s) : 0.0;
-        z = z > 15.0 ? 15.0 : z;
-    }
+    const float s = (float)st;
+    float z = 8.0f;
+    if (asym) z = s > 0.0f ? fminf((float)rint(-(double)lo / (double)s), 15.0f) : 0.0f;
     if (lane == 0) {
         ((T*)a.S)[row * a.lds + g] = st;
-        if (asym) ((T*)a.Z)[row * a.ldz + g] = (T)(float)z;
+        if (asym) ((T*)a.Z)[row * a.ldz + g] = (T)z;
     }
+    // No scale (0 or NaN): every number is the zero point.
+    const bool flat = !(s > 0.0f);
+    const float inv = flat ? 0.0f : 1.0f / s;
+    const bool far = !(inv <= 3.0e38f);   // 1 / s overflows: only the 64-bit quotient serves
     uint8_t* q = a.Q + row * a.ldq;
     for (int k = k0 + 2 * lane; k < k1; k += 128) {
-        const uint32_t q0 = quantise((float)w[k], s, z);
-        const uint32_t q1 = k + 1 < a.K ? quantise((float)w[k + 1], s, z) : 0u;
-        q[k >> 1] = (uint8_t)(q0 | (q1 << 4));
+        uint32_t v[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (k + e >= a.K) break;
+            const float x = (float)w[k + e];
+            if (flat)
+                v[e] = (uint32_t)(int)z;
+            else if (far)
+                v[e] = (uint32_t)(int)fmin(fmax(rint((double)x / (double)s) + z, 0.0), 15.0);
+            else
+                v[e] = quantise(x, s, inv, z);
+        }
+        q[k >> 1] = (uint8_t)(v[0] | (v[1] << 4));
     }
 }
 
