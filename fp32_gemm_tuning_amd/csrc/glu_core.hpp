@@ -296,8 +296,10 @@ struct DmaFill {
     int q[G];          // KC: first k of the chunk
 
     // PAIR: which of the two matrices piece p of wave w (8 rows) belongs to.
-    static_assert(W == 4 || W % 8 == 0, "a piece's matrix depends on the wave or on p alone");
-    __device__ __forceinline__ static int matrix(int w, int p) { return W == 4 ? p & 1 : (w >> 2) & 1; }
+    static_assert(W == 1 || W == 4 || W % 8 == 0, "a piece's matrix depends on the wave or on p alone");
+    __device__ __forceinline__ static int matrix(int w, int p) {
+        return W == 1 ? (p >> 2) & 1 : W == 4 ? p & 1 : (w >> 2) & 1;
+    }
 
     // A KC tile's rows start at line r0 (PAIR: of both matrices, as in
     // RegFill), an RC tile's chunks at element r0 of each line.
@@ -452,5 +454,15 @@ struct DmaCore {
         ring_barrier<0>();   // the loads past the last slice land before LDS is given up
     }
 };
+
+// Waits until at most VMCNT of this wave's vector-memory operations are
+// outstanding (their LDS writes included); nothing moves across.
+template <int VMCNT>
+__device__ __forceinline__ void wave_wait() {
+    static_assert(VMCNT >= 0 && VMCNT < 64, "vmcnt field is 6 bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((VMCNT & 15) | ((VMCNT >> 4) << 14) | (7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
+}
 
 }  // namespace sgemm

@@ -66,6 +66,113 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_fwd(GluArgs a, int tiles_m, int 
     });
 }
 
+// The forward pass of few rows: the weights' bytes are the work. A workgroup takes
+// BM rows of X and 32 features; its KW waves take K's slices in turn, each with a
+// ring of LDS stages of its own, so no wave waits for another before the sums
+// are added in wave order at the end. Three stages keep two slices of every wave
+// in flight (96 KiB a compute unit at BM = 32).
+constexpr int KW = 4;
+template <class T, int BM, bool DMA, bool SHORT>
+__global__ __launch_bounds__(KW * 64) void k_glu_rows(GluArgs a) {
+    constexpr int BN = 64, BI = BM / 32, STAGES = DMA && BM == 32 ? 3 : 2, STAGE = (BM + BN) * 128;
+    static_assert(STAGES * STAGE >= BI * 2 * 16 * 64 * 4, "the sums fit in the rings");
+    __shared__ __attribute__((aligned(16))) char lds[KW * STAGES * STAGE];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int f0 = blockIdx.x * 32, m0 = blockIdx.y * BM;
+    const int nslices = (a.K + Elem<T>::SLICE - 1) / Elem<T>::SLICE;
+    const int count = nslices > w ? (nslices - w + KW - 1) / KW : 0;
+    char* const ring = lds + w * (STAGES * STAGE);
+    const Lines<T> x = {(const T*)a.X, a.ldx, a.M, a.K};
+    const Lines<T> wgt[2] = {{(const T*)a.Wg, a.ldwg, a.F, a.K}, {(const T*)a.Wu, a.ldwu, a.F, a.K}};
+    f32x16 acc[BI][2];
+#pragma unroll
+    for (int i = 0; i < BI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    auto compute = [&](const char* A) {
+        const char* B = A + BM * 128;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const i32x4 g = read_frag<T, BN, false>(B, 0, lane, v), u = read_frag<T, BN, false>(B, 32, lane, v);
+#pragma unroll
+            for (int i = 0; i < BI; ++i) {
+                const i32x4 xv = read_frag<T, BM, false>(A, 32 * i, lane, v);
+                mma_chunk(T{}, xv, g, acc[i][0]);
+                mma_chunk(T{}, xv, u, acc[i][1]);
+            }
+        }
+    };
+    auto k_of = [&](int i) { return (w + KW * i) * Elem<T>::SLICE; };
+    if constexpr (DMA) {
+        DmaFill<T, BM, 64, false> fa;
+        DmaFill<T, BN, 64, false> fb;
+        fa.template init<false>(&x, m0, lane);
+        fb.template init<true>(wgt, f0, lane);
+        auto issue = [&](int i, char* st) {   // slices past K read as zeros
+            fa.template issue<false>(&x, m0, k_of(i), lane, st);
+            fb.template issue<true>(wgt, f0, k_of(i), lane, st + BM * 128);
+        };
+        if (count > 0) {
+#pragma unroll
+            for (int i = 0; i < STAGES - 1; ++i) issue(i, ring + i * STAGE);
+            int at = 0;
+            for (int i = 0; i < count; ++i) {
+                const int to = at == 0 ? STAGES - 1 : at - 1;   // the stage read one slice ago
+                issue(i + STAGES - 1, ring + to * STAGE);
+                wave_wait<(STAGES - 1) * (decltype(fa)::G + decltype(fb)::G)>();
+                compute(ring + at * STAGE);
+                at = at == STAGES - 1 ? 0 : at + 1;
+            }
+            wave_wait<0>();
+        }
+    } else if (count > 0) {
+        RegFill<T, BM, 64, false, SHORT> fa;
+        RegFill<T, BN, 64, false, SHORT> fb;
+        auto load = [&](int i) {
+            fa.template load<false>(&x, m0, k_of(i), lane);
+            fb.template load<true>(wgt, f0, k_of(i), lane);
+        };
+        load(0);
+        for (int i = 0; i < count; ++i) {
+            char* st = ring + (i & 1) * STAGE;
+            fa.template store<false>(st, &x, m0, k_of(i), lane);
+            fb.template store<true>(st + BM * 128, wgt, f0, k_of(i), lane);
+            load(i + 1 < count ? i + 1 : i);
+            compute(st);
+        }
+    }
+    // Sums over the waves in their order.
+    __syncthreads();
+    float* const red = (float*)lds;
+    constexpr int PER_WAVE = STAGES * STAGE / 4;
+#pragma unroll
+    for (int i = 0; i < BI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) red[w * PER_WAVE + ((i * 2 + j) * 16 + r) * 64 + lane] = acc[i][j][r];
+    __syncthreads();
+#pragma unroll
+    for (int o = 0; o < BI * 16 / KW; ++o) {
+        const int ir = w * (BI * 16 / KW) + o, i = ir >> 4, r = ir & 15;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int ww = 0; ww < KW; ++ww) {
+            g += red[ww * PER_WAVE + (i * 32 + r) * 64 + lane];
+            u += red[ww * PER_WAVE + (i * 32 + 16 + r) * 64 + lane];
+        }
+        const int row = m0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), f = f0 + (lane & 31);
+        if (row >= a.M || f >= a.F) continue;
+        ((T*)a.H)[(int64_t)row * a.ldh + f] = (T)(act_value(a.act, g) * u);
+        if (a.P != nullptr) {
+            a.P[(int64_t)row * a.ldp + f] = g;
+            a.P[(int64_t)row * a.ldp + a.F + f] = u;
+        }
+    }
+}
+
 // dX = dG Wg + dU Wu as one sum over 2F: first the slices of dG and Wg, then
 // those of dU and Wu.
 template <class T, class Tl>
@@ -141,11 +248,25 @@ int check_glu(const GluArgs& a) {
     return tiles <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
+template <class T, int BM>
+static hipError_t launch_glu_rows(const GluArgs& a, bool dma, hipStream_t s) {
+    const dim3 grid((unsigned)cdiv(a.F, 32), (unsigned)cdiv(a.M, BM));
+    if (a.K < Elem<T>::EPC)
+        hipLaunchKernelGGL((k_glu_rows<T, BM, false, true>), grid, dim3(KW * 64), 0, s, a);
+    else if (dma)
+        hipLaunchKernelGGL((k_glu_rows<T, BM, true, false>), grid, dim3(KW * 64), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_glu_rows<T, BM, false, false>), grid, dim3(KW * 64), 0, s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s) {
     const bool dma = dma_ok(dtype, a.X, a.ldx, a.K, 256) && dma_ok(dtype, a.Wg, a.ldwg, a.K, 128) &&
                      dma_ok(dtype, a.Wu, a.ldwu, a.K, 128);
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
+        if (a.M <= 32) return launch_glu_rows<T, 32>(a, dma, s);
+        if (a.M <= 64) return launch_glu_rows<T, 64>(a, dma, s);
         return with_tile(dtype, a.K, dma, a.M, 2 * (int64_t)a.F, 1, [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.F, Tl::BN / 2);

@@ -29,6 +29,7 @@ that is not given is allocated:
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional, Tuple
 
 from . import SgemmError, _lib, _ptr, _stream
@@ -68,6 +69,7 @@ def sgemm_f32_glu_bwd(dtype, act, M, F, K, X, ldx, Wg, ldwg, Wu, ldwu, P, ldp, d
                                   _ptr(workspace), workspace_bytes, _stream(stream, dH, X))
 
 
+@functools.lru_cache(maxsize=256)
 def sgemm_f32_glu_bwd_ws_size(dtype, M, F, K, num_cus) -> Tuple[int, int]:
     b = ctypes.c_size_t(0)
     rc = _lib.sgemm_f32_glu_bwd_ws_size(dtype, M, F, K, num_cus, ctypes.byref(b))
@@ -110,11 +112,15 @@ class W4(NamedTuple):
 
 
 _dtypes = {}
+_raw_stream = None   # device index -> address of its current stream
 
 
 def _dtype(t, name: str) -> int:
+    global _raw_stream
     if not _dtypes:
         import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
         _dtypes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
     d = _dtypes.get(t.dtype)
     if d is None:
@@ -131,9 +137,13 @@ def _act(act) -> int:
 
 def _ld(t, like, dtype, rows: int, cols: int, name: str) -> int:
     """The leading dimension of a rows x cols matrix on `like`'s device."""
+    if t.dtype is dtype and t.get_device() == like.get_device() and t.shape == (rows, cols):
+        sr, sc = t.stride()
+        if rows > 1 and sr >= cols > 0 and (sc == 1 or cols == 1):
+            return sr
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.dim() != 2 or t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape ({rows}, {cols}), got {tuple(t.shape)}")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, not on {like.device}")
@@ -155,14 +165,18 @@ def _gpu(t, name: str):
     return _dtype(t, name)
 
 
+_entries = {name: getattr(_lib, name) for name in _SIGNATURES}
+
+
 def _call(like, stream, entry: str, *args) -> None:
     """Calls the C entry point with `like`'s device current."""
     import torch
-    if torch.cuda.current_device() == like.device.index:
-        rc = getattr(_lib, entry)(*args, _stream(stream, like))
+    index = like.get_device()
+    if torch.cuda.current_device() == index:
+        rc = _entries[entry](*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(like.device):
-            rc = getattr(_lib, entry)(*args, _stream(stream, like))
+        with torch.cuda.device(index):
+            rc = _entries[entry](*args, _raw_stream(index) if stream is None else _stream(stream))
     if rc != 0:
         raise SgemmError(rc, entry)
 
@@ -229,10 +243,10 @@ _cus = {}
 def glu_backward_workspace(X, F: int) -> int:
     """Bytes of workspace glu_backward needs for X (M, K) and F features."""
     d = _gpu(X, "X")
-    cus = _cus.get(X.device)
+    cus = _cus.get(X.get_device())
     if cus is None:
         import torch
-        cus = _cus[X.device] = torch.cuda.get_device_properties(X.device).multi_processor_count
+        cus = _cus[X.get_device()] = torch.cuda.get_device_properties(X.device).multi_processor_count
     rc, need = sgemm_f32_glu_bwd_ws_size(d, X.shape[0], F, X.shape[1], cus)
     if rc != 0:
         raise SgemmError(rc, "sgemm_f32_glu_bwd_ws_size")
