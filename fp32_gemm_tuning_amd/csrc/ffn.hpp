@@ -91,12 +91,14 @@ struct GluGradArgs {
 
 // A 16-bit product of the backward pass. dX: C0 = dG W[0] + dU W[1]; dW:
 // C0 = dG^T X, C1 = dU^T X (either may be null). D are dG and dU (M x F,
-// leading dimension ldd).
+// leading dimension ldd); part is the space of split products' partial sums
+// (glu_prod_bytes).
 struct GluProdArgs {
     const void* D[2];
     const void* W[2];
     const void* X;
     void* C[2];
+    float* part;
     int64_t ldd, ldw[2], ldx, ldc[2];
     int32_t M, F, K;
 };
@@ -128,6 +130,7 @@ struct PackArgs {
 int check_glu(const GluArgs& a);
 hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s);
 int check_glu_prod(const GluProdArgs& a);
+size_t glu_prod_bytes(int64_t M, int64_t F, int64_t K);
 hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s);
 hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s);
 // glu_grad.hip

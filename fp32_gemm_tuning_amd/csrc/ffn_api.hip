@@ -41,7 +41,8 @@ int32_t group_of(int64_t group, int64_t K) {
 
 // The backward pass's workspace: dG and dU, each M rows of ldd elements (F
 // rounded up to whole 64-element slices, so that their rows are whole 16-byte
-// chunks), then, for FP32, what the stream-K kernels of its products may use.
+// chunks), then, for FP32, what the stream-K kernels of its products may use, or
+// the partial sums of 16-bit products that are split.
 struct BwdSpace {
     int64_t ldd;
     size_t du_at, sk_at, sk_bytes, total;
@@ -61,6 +62,8 @@ int bwd_space(int dtype, int64_t M, int64_t F, int64_t K, int num_cus, BwdSpace*
                                    num_cus, &dw);
         if (rc) return rc;
         o->sk_bytes = up256(dx > dw ? dx : dw);
+    } else {
+        o->sk_bytes = up256(glu_prod_bytes(M, F, K));
     }
     o->total = o->sk_at + o->sk_bytes;
     return 0;
@@ -201,7 +204,7 @@ SGEMM_F32_API int sgemm_f32_glu_bwd(int dtype, int act, int64_t M, int64_t F, in
     char* const ws = (char*)workspace;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
 
-    GluProdArgs p = {{ws, ws + sp.du_at}, {Wg, Wu}, X, {nullptr, nullptr}, sp.ldd, {ldwg, ldwu}, ldx,
+    GluProdArgs p = {{ws, ws + sp.du_at}, {Wg, Wu}, X, {nullptr, nullptr}, (float*)(ws + sp.sk_at), sp.ldd, {ldwg, ldwu}, ldx,
                      {0, 0}, (int32_t)M, (int32_t)F, (int32_t)K};
     const GluGradArgs g = {P, dH, ws, ws + sp.du_at, ldp, lddh, sp.ldd, (int32_t)M, (int32_t)F, act};
     rc = check_glu_grad(g);

@@ -194,8 +194,11 @@ __device__ __forceinline__ i32x4 read_frag(const char* lds, int row0, int lane, 
 }
 
 // The product of one tile: BM x BN outputs, waves of WM x WN, both operands
-// through registers into two LDS stages. `nslices` slices; slice s takes its
-// operands from sources src(s, A sources, B sources) -> first k.
+// through registers into two LDS stages. src(s, A, B[2]) gives slice s's
+// operands and returns its first k; slices s_begin .. s_end - 1 are summed. Two
+// register sets keep the loads of the next two slices in flight (a slice's
+// products are shorter than a load's way from memory), and the barrier waits for
+// LDS only.
 template <class T, int BM, int BN, int WM, int WN, bool ARC, bool BRC, bool PAIR, bool SHORT = false>
 struct TileCore {
     static constexpr int WAVES_N = BN / WN;
@@ -204,7 +207,7 @@ struct TileCore {
     static constexpr int STAGE = (BM + BN) * 128;
 
     template <class Src>
-    __device__ __forceinline__ static void run(char* lds, int m0, int n0, int nslices, Src&& src,
+    __device__ __forceinline__ static void run(char* lds, int m0, int n0, int s_begin, int s_end, Src&& src,
                                                f32x16 (&acc)[BI][BJ]) {
         const int t = threadIdx.x, lane = t & 63, w = t >> 6;
         const int wm = (w / WAVES_N) * WM, wn = (w % WAVES_N) * WN;
@@ -214,27 +217,25 @@ struct TileCore {
             for (int j = 0; j < BJ; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-        if (nslices <= 0) return;
-        RegFill<T, BM, NT, ARC, SHORT> fa;
-        RegFill<T, BN, NT, BRC, SHORT> fb;
-        Lines<T> la, lb[2];   // of the slice in flight
-        int k0 = 0;
-        auto load = [&](int s) {
-            k0 = src(s, la, lb);
-            fa.template load<false>(&la, m0, k0, t);
-            fb.template load<PAIR>(lb, n0, k0, t);
+        if (s_begin >= s_end) return;
+        struct Set {
+            RegFill<T, BM, NT, ARC, SHORT> a;
+            RegFill<T, BN, NT, BRC, SHORT> b;
         };
-        auto store = [&](int s) {
-            char* st = lds + (s & 1) * STAGE;
-            fa.template store<false>(st, &la, m0, k0, t);
-            fb.template store<PAIR>(st + BM * 128, lb, n0, k0, t);
+        // Past the last slice the last one is loaded (and stored) again.
+        auto load = [&](int s, Set& r) {
+            Lines<T> la, lb[2];
+            const int k0 = src(s < s_end ? s : s_end - 1, la, lb);
+            r.a.template load<false>(&la, m0, k0, t);
+            r.b.template load<PAIR>(lb, n0, k0, t);
         };
-        load(0);
-        store(0);
-        __syncthreads();
-        for (int s = 0; s < nslices; ++s) {
-            if (s + 1 < nslices) load(s + 1);
-            const char* A = lds + (s & 1) * STAGE;
+        auto store = [&](int s, const Set& r, char* st) {
+            Lines<T> la, lb[2];
+            const int k0 = src(s < s_end ? s : s_end - 1, la, lb);
+            r.a.template store<false>(st, &la, m0, k0, t);
+            r.b.template store<PAIR>(st + BM * 128, lb, n0, k0, t);
+        };
+        auto compute = [&](const char* A) {
             const char* B = A + BM * 128;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
@@ -248,10 +249,27 @@ struct TileCore {
 #pragma unroll
                     for (int j = 0; j < BJ; ++j) mma_chunk(T{}, a[i], b[j], acc[i][j]);
             }
-            // The other stage was last read before the previous barrier.
-            if (s + 1 < nslices) store(s + 1);
-            __syncthreads();
+        };
+        Set r0, r1;
+        load(s_begin, r0);
+        load(s_begin + 1, r1);
+        store(s_begin, r0, lds);
+        load(s_begin + 2, r0);
+        ring_barrier<63>();
+        // The stage written was last read before the previous barrier.
+        auto slice = [&](int s, char* now, char* next, Set& r) {
+            compute(now);
+            __builtin_amdgcn_sched_barrier(0);
+            store(s + 1, r, next);
+            load(s + 3, r);
+            ring_barrier<63>();
+        };
+        int s = s_begin;
+        for (; s + 2 <= s_end; s += 2) {
+            slice(s, lds, lds + STAGE, r1);
+            slice(s + 1, lds + STAGE, lds, r0);
         }
+        if (s < s_end) compute(lds);
     }
 
     // f(i, j, register values of block (bi, bj) at tile row i, tile column j).
@@ -296,9 +314,9 @@ struct DmaFill {
     int q[G];          // KC: first k of the chunk
 
     // PAIR: which of the two matrices piece p of wave w (8 rows) belongs to.
-    static_assert(W == 1 || W == 4 || W % 8 == 0, "a piece's matrix depends on the wave or on p alone");
+    static_assert(W == 1 || W == 2 || W == 4 || W % 8 == 0, "a piece's matrix depends on the wave or on p alone");
     __device__ __forceinline__ static int matrix(int w, int p) {
-        return W == 1 ? (p >> 2) & 1 : W == 4 ? p & 1 : (w >> 2) & 1;
+        return W <= 4 ? (W * p >> 2) & 1 : (w >> 2) & 1;
     }
 
     // A KC tile's rows start at line r0 (PAIR: of both matrices, as in
@@ -371,7 +389,7 @@ struct DmaCore {
         constexpr int MFMA = 0x008, VMEM_READ = 0x020, DS_READ = 0x100;
         constexpr int MFMAS = BI * BJ * (sizeof(T) == 4 ? 4 : 1);
         constexpr int READS = BI * (ARC ? 2 : 1) + BJ * (BRC ? 2 : 1);
-        constexpr int RS = (READS + MFMAS - 3) / (MFMAS - 2);   // reads after each of the first ones
+        constexpr int RN = MFMAS > 2 ? MFMAS - 2 : 1, RS = (READS + RN - 1) / RN;   // reads after each of the first RN
         constexpr int LS = LOADS == 0 ? 1 : (LOADS + MFMAS - 2) / (MFMAS - 1);
 #pragma unroll
         for (int i = 0; i < MFMAS; ++i) {
@@ -384,7 +402,7 @@ struct DmaCore {
     // src(s, A, B[2]) -> first k of slice s, with the operands' lines.
     template <class Src>
     __device__ __forceinline__ static void run(char* a0, char* b0, char* a1, char* b1, int m0, int n0,
-                                               int nslices, Src&& src, f32x16 (&acc)[BI][BJ]) {
+                                               int s_begin, int s_end, Src&& src, f32x16 (&acc)[BI][BJ]) {
         const int t = threadIdx.x, lane = t & 63, w = t >> 6;
         const int wm = (w / WAVES_N) * WM, wn = (w % WAVES_N) * WN;
 #pragma unroll
@@ -393,12 +411,12 @@ struct DmaCore {
             for (int j = 0; j < BJ; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-        if (nslices <= 0) return;
+        if (s_begin >= s_end) return;
         FA fa;
         FB fb;
         {
             Lines<T> la, lb[2];
-            src(0, la, lb);
+            src(s_begin, la, lb);
             fa.template init<false>(&la, m0, t);
             fb.template init<PAIR>(lb, n0, t);
         }
@@ -421,8 +439,8 @@ struct DmaCore {
                 for (int j = 0; j < BJ; ++j) mma_chunk(T{}, f.a[i], f.b[j], acc[i][j]);
         };
         Frag f0, f1;
-        issue(0, a0, b0);
-        issue(1, a1, b1);   // past the last slice: zeros, never used
+        issue(s_begin, a0, b0);
+        issue(s_begin + 1, a1, b1);   // past the last slice: never used
         ring_barrier<FA::G + FB::G>();
         read(f0, a0, b0, 0);
         auto slice = [&](int s, char* A, char* B, char* An, char* Bn) {
@@ -445,12 +463,12 @@ struct DmaCore {
             weave<FA::G + FB::G>();
             __builtin_amdgcn_sched_barrier(0);
         };
-        int s = 0;
-        for (; s + 2 <= nslices; s += 2) {
+        int s = s_begin;
+        for (; s + 2 <= s_end; s += 2) {
             slice(s, a0, b0, a1, b1);
             slice(s + 1, a1, b1, a0, b0);
         }
-        if (s < nslices) slice(s, a0, b0, a1, b1);
+        if (s < s_end) slice(s, a0, b0, a1, b1);
         ring_barrier<0>();   // the loads past the last slice land before LDS is given up
     }
 };

@@ -5,25 +5,48 @@
 
 namespace sgemm {
 
-// One thread per element of the M x ldd results; columns from F on are zero.
+// Four consecutive columns a thread (ldd is a multiple of 64, so four
+// never straddle a row of the results; loads need only element alignment).
+// Bound by its bytes: P and dH read, dG and dU written.
 template <class T>
 __global__ __launch_bounds__(256) void k_glu_grad(GluGradArgs a) {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    typedef T4 T4u __attribute__((aligned(sizeof(T))));
+    typedef f32x4 F4u __attribute__((aligned(4)));
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     const int64_t row = at / a.ldd;
     const int col = (int)(at - row * a.ldd);
     if (row >= a.M) return;
-    float dg = 0.0f, du = 0.0f;
-    if (col < a.F) {
-        const float g = a.P[row * a.ldp + col], u = a.P[row * a.ldp + a.F + col];
-        const float dh = (float)((const T*)a.dH)[row * a.lddh + col];
-        du = dh * act_value(a.act, g);
-        dg = dh * u * act_slope(a.act, g);
+    T4 dg = {}, du = {};
+    const float* p = a.P + row * a.ldp + col;
+    const T* h = (const T*)a.dH + row * a.lddh + col;
+    f32x4 g = {}, u = {};
+    T4 dh = {};
+    if (col + 4 <= a.F) {
+        g = *(const F4u*)p;
+        u = *(const F4u*)(p + a.F);
+        dh = *(const T4u*)h;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < a.F) {
+                g[e] = p[e];
+                u[e] = p[a.F + e];
+                dh[e] = h[e];
+            }
     }
-    ((T*)a.dG)[at] = (T)dg;
-    ((T*)a.dU)[at] = (T)du;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (col + e >= a.F) break;
+        const float d = (float)dh[e];
+        du[e] = (T)(d * act_value(a.act, g[e]));
+        dg[e] = (T)(d * u[e] * act_slope(a.act, g[e]));
+    }
+    *(T4*)((T*)a.dG + at) = dg;
+    *(T4*)((T*)a.dU + at) = du;
 }
 
-static int64_t workgroups(const GluGradArgs& a) { return ((int64_t)a.M * a.ldd + 255) / 256; }
+static int64_t workgroups(const GluGradArgs& a) { return ((int64_t)a.M * a.ldd / 4 + 255) / 256; }
 
 int check_glu_grad(const GluGradArgs& a) {
     return workgroups(a) <= max_workgroups(256) ? 0 : SGEMM_F32_ERR_TOO_LARGE;

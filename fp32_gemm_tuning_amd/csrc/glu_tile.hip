@@ -12,15 +12,15 @@ constexpr int GLU_GROUP_M = 8;
 // apart so that the compiler can tell the stage being filled from the one
 // being read.
 template <class Core, bool DMA, class Src>
-__device__ __forceinline__ void product(int m0, int n0, int nslices, Src&& src,
+__device__ __forceinline__ void product(int m0, int n0, int s_begin, int s_end, Src&& src,
                                         f32x16 (&acc)[Core::BI][Core::BJ]) {
     if constexpr (DMA) {
         __shared__ __attribute__((aligned(16))) char a0[Core::LDS_A], b0[Core::LDS_B], a1[Core::LDS_A],
             b1[Core::LDS_B];
-        Core::run(a0, b0, a1, b1, m0, n0, nslices, src, acc);
+        Core::run(a0, b0, a1, b1, m0, n0, s_begin, s_end, src, acc);
     } else {
         __shared__ __attribute__((aligned(16))) char lds[2 * Core::STAGE];
-        Core::run(lds, m0, n0, nslices, src, acc);
+        Core::run(lds, m0, n0, s_begin, s_end, src, acc);
     }
 }
 
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_fwd(GluArgs a, int tiles_m, int 
         lb[1] = Lines<T>{(const T*)a.Wu, a.ldwu, a.F, a.K};
         return s * Elem<T>::SLICE;
     };
-    product<Core, Tl::DMA>(m0, f0, (a.K + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
+    product<Core, Tl::DMA>(m0, f0, 0, (a.K + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
     TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, false, false, true>::each([&](int bi, int bj, int r, int i, int j) {
         if (bj & 1) return;
         const int row = m0 + i, f = f0 + (j >> 6) * 32 + (j & 31);
@@ -173,15 +173,32 @@ __global__ __launch_bounds__(KW * 64) void k_glu_rows(GluArgs a) {
     }
 }
 
+// Where a backward product's sums go: the result, or, split over its slices
+// (blockIdx.z of gridDim.z parts), FP32 partial sums that k_glu_sum adds in order.
+template <class T>
+__device__ __forceinline__ void put(const GluProdArgs& a, int u, int64_t rows, int row, int col, float v) {
+    if (gridDim.z > 1)
+        a.part[((int64_t)(blockIdx.z * gridDim.y + blockIdx.y) * rows + row) * a.K + col] = v;
+    else
+        ((T*)(u ? a.C[1] : a.C[0]))[(int64_t)row * (u ? a.ldc[1] : a.ldc[0]) + col] = (T)v;
+}
+// This part's slices of n.
+__device__ __forceinline__ void part_of(int n, int& begin, int& end) {
+    const int per = (n + gridDim.z - 1) / gridDim.z;
+    begin = blockIdx.z * per < n ? blockIdx.z * per : n;
+    end = begin + per < n ? begin + per : n;
+}
+
 // dX = dG Wg + dU Wu as one sum over 2F: first the slices of dG and Wg, then
 // those of dU and Wu.
 template <class T, class Tl>
 __global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, int tiles_n, int xcd) {
     using Core = typename Tl::template Core<T, false, true, false>;
-    int tm, tn;
+    int tm, tn, s0, s1;
     tile_of(blockIdx.x, tiles_m, tiles_n, GLU_GROUP_M, xcd != 0, tm, tn);
     const int m0 = __builtin_amdgcn_readfirstlane(tm * Tl::BM), n0 = __builtin_amdgcn_readfirstlane(tn * Tl::BN);
     const int half = (a.F + Elem<T>::SLICE - 1) / Elem<T>::SLICE;
+    part_of(2 * half, s0, s1);
     f32x16 acc[Core::BI][Core::BJ];
     auto src = [&](int s, Lines<T>& la, Lines<T>* lb) {
         const int u = s >= half;
@@ -191,10 +208,10 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, i
         if (!Tl::DMA) lb[0].ld = u ? a.ldw[1] : a.ldw[0];
         return (s - u * half) * Elem<T>::SLICE;
     };
-    product<Core, Tl::DMA>(m0, n0, 2 * half, src, acc);
+    product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
     TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, false, true, false>::each([&](int bi, int bj, int r, int i, int j) {
         const int row = m0 + i, col = n0 + j;
-        if (row < a.M && col < a.K) ((T*)a.C[0])[(int64_t)row * a.ldc[0] + col] = (T)acc[bi][bj][r];
+        if (row < a.M && col < a.K) put<T>(a, 0, a.M, row, col, acc[bi][bj][r]);
     });
 }
 
@@ -203,24 +220,38 @@ template <class T, class Tl>
 __global__ __launch_bounds__(Tl::NT) void k_glu_dw(GluProdArgs a, int tiles_m, int tiles_n, int xcd) {
     using Core = typename Tl::template Core<T, true, true, false>;
     const int u = a.C[0] == nullptr ? 1 : blockIdx.y;
-    int tm, tn;
+    int tm, tn, s0, s1;
     tile_of(blockIdx.x, tiles_m, tiles_n, GLU_GROUP_M, xcd != 0, tm, tn);
     const int m0 = __builtin_amdgcn_readfirstlane(tm * Tl::BM), n0 = __builtin_amdgcn_readfirstlane(tn * Tl::BN);
+    part_of((a.M + Elem<T>::SLICE - 1) / Elem<T>::SLICE, s0, s1);
     f32x16 acc[Core::BI][Core::BJ];
     auto src = [&](int s, Lines<T>& la, Lines<T>* lb) {
         la = Lines<T>{(const T*)(u ? a.D[1] : a.D[0]), a.ldd, a.M, (a.F + 63) / 64 * 64};
         lb[0] = Lines<T>{(const T*)a.X, a.ldx, a.M, a.K};
         return s * Elem<T>::SLICE;
     };
-    product<Core, Tl::DMA>(m0, n0, (a.M + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
+    product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
     TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, true, true, false>::each([&](int bi, int bj, int r, int i, int j) {
         const int f = m0 + i, col = n0 + j;
-        T* const C = (T*)(u ? a.C[1] : a.C[0]);
-        if (f < a.F && col < a.K) C[(int64_t)f * (u ? a.ldc[1] : a.ldc[0]) + col] = (T)acc[bi][bj][r];
+        if (f < a.F && col < a.K) put<T>(a, u, a.F, f, col, acc[bi][bj][r]);
     });
 }
 
+// The sums of a split product's parts, in their order.
+template <class T>
+__global__ __launch_bounds__(256) void k_glu_sum(GluProdArgs a, int rows, int parts) {
+    const int64_t n = (int64_t)rows * a.K, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= n) return;
+    const int u = a.C[0] == nullptr ? 1 : blockIdx.y;
+    float v = 0.0f;
+    for (int z = 0; z < parts; ++z) v += a.part[((int64_t)z * gridDim.y + blockIdx.y) * n + at];
+    const int64_t row = at / a.K;
+    ((T*)(u ? a.C[1] : a.C[0]))[row * (u ? a.ldc[1] : a.ldc[0]) + (at - row * a.K)] = (T)v;
+}
+
 using TileReg = Tile<128, 128, 64, 64, false>;
+using TileReg64 = Tile<64, 64, 32, 64, false>;
+using TileDma64 = Tile<64, 64, 32, 64, true>;
 using TileShort = Tile<128, 128, 64, 64, false, true>;
 using TileMid = Tile<128, 128, 64, 64, true>;
 using TileBig = Tile<256, 256, 128, 64, true>;
@@ -233,18 +264,66 @@ static bool dma_ok(int dtype, const void* p, int64_t ld, int64_t extent, int64_t
            ((tile_lines - 1) * ld + extent) * e < (int64_t)kRange;
 }
 
-// f(tile tag): the register-filled tile where an operand is not whole
-// chunks, else the big tile where it gives every compute unit work.
+// Times that the choice of a tile goes by, in microseconds, measured on MI355X
+// (products of 512 x 2048 x 2048 to 4096 x 8192 x 4096): a call takes about
+//     fixed + n max(alone, tiles per compute unit * busy)
+// for n slices, with `alone` a slice of a lone tile and `busy` a slice's share of a
+// unit that holds several. FP32 slices hold half the k and take the matrix
+// cores eight times as long.
+struct TileCost {
+    double fixed, alone, busy;
+    double of(int64_t tiles, int64_t slices) const {
+        const double per_unit = (double)((tiles + 255) / 256), b = per_unit * busy;
+        return fixed + (double)slices * (b > alone ? b : alone);
+    }
+};
+static const TileCost kBig[2] = {{9.0, 1.8, 1.8}, {9.0, 7.3, 7.3}};
+static const TileCost kMid[2] = {{7.0, 0.45, 0.52}, {7.0, 2.2, 2.0}};
+static const TileCost k64[2] = {{6.0, 0.28, 0.19}, {6.0, 0.70, 0.66}};
+
+// f(tile tag): the tile that the model above finds fastest; filled through registers
+// where an operand is not whole chunks (never the big tile: its registers
+// are taken). `split`: the product is split, which the 64 x 64 tiles do.
 template <class Fn>
-static hipError_t with_tile(int dtype, int K, bool dma, int64_t rows, int64_t cols, int64_t copies, Fn&& f) {
+static hipError_t with_tile(int dtype, int K, bool dma, bool split, int64_t rows, int64_t cols, int64_t copies,
+                            int64_t slices, Fn&& f) {
+    const int f32 = dtype == SGEMM_F32_DTYPE_F32;
     if (K < 16 / dtype_bytes(dtype)) return f(TypeTag<TileShort>{});
+    auto tiles = [&](int64_t b) { return cdiv(rows, b) * cdiv(cols, b) * copies; };
+    const double c64 = k64[f32].of(tiles(64), slices), cmid = kMid[f32].of(tiles(128), slices);
+    const double cbig = kBig[f32].of(tiles(256), slices);
+    if (split || (c64 < cmid && (!dma || c64 < cbig)))
+        return dma ? f(TypeTag<TileDma64>{}) : f(TypeTag<TileReg64>{});
     if (!dma) return f(TypeTag<TileReg>{});
-    if (cdiv(rows, 256) * cdiv(cols, 256) * copies >= 192) return f(TypeTag<TileBig>{});
+    if (cbig < cmid) return f(TypeTag<TileBig>{});
     return f(TypeTag<TileMid>{});
 }
 
+// Parts that a product of few tiles is split into: as many as make 512 of the
+// 64 x 64 tiles, of at least four slices each. By sizes alone, so that the
+// workspace's size does not depend on alignment.
+static int parts(int64_t rows, int64_t cols, int64_t copies, int64_t slices, int K) {
+    const int64_t tiles = cdiv(rows, 64) * cdiv(cols, 64) * copies;
+    if (tiles >= 256 || K < 8) return 1;
+    const int64_t by_tiles = 512 / tiles, by_slices = slices / 4, n = by_tiles < by_slices ? by_tiles : by_slices;
+    return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+}
+static int dx_parts(int64_t M, int64_t F, int64_t K) { return parts(M, K, 1, 2 * cdiv(F, 64), (int)K); }
+static int dw_parts(int64_t M, int64_t F, int64_t K, int copies) { return parts(F, K, copies, cdiv(M, 64), (int)K); }
+size_t glu_prod_bytes(int64_t M, int64_t F, int64_t K) {
+    if (M == 0 || F == 0 || K == 0) return 0;
+    size_t most = 0;
+    const int dx = dx_parts(M, F, K);
+    if (dx > 1) most = (size_t)dx * M * K * 4;
+    for (int c = 1; c <= 2; ++c) {
+        const int dw = dw_parts(M, F, K, c);
+        if (dw > 1 && (size_t)dw * c * F * K * 4 > most) most = (size_t)dw * c * F * K * 4;
+    }
+    return most;
+}
+
 int check_glu(const GluArgs& a) {
-    const int64_t tiles = cdiv(a.M, 128) * cdiv(a.F, 64);
+    const int64_t tiles = cdiv(a.M, 64) * cdiv(a.F, 32);
     return tiles <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
@@ -265,9 +344,12 @@ hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s) {
                      dma_ok(dtype, a.Wu, a.ldwu, a.K, 128);
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        if (a.M <= 32) return launch_glu_rows<T, 32>(a, dma, s);
-        if (a.M <= 64) return launch_glu_rows<T, 64>(a, dma, s);
-        return with_tile(dtype, a.K, dma, a.M, 2 * (int64_t)a.F, 1, [&](auto tile) {
+        // Few rows, or few tiles: the workgroups that split K (128 x 4096 x 4096
+        // bf16 21 us against 35 on 64 x 64 tiles, 512 x 2048 x 2048 level).
+        const int64_t wgs64 = cdiv(a.M, 64) * cdiv(a.F, 32), wgs32 = cdiv(a.M, 32) * cdiv(a.F, 32);
+        if (a.M <= 32 || wgs32 <= 256) return launch_glu_rows<T, 32>(a, dma, s);
+        if (a.M <= 64 || wgs64 <= 256) return launch_glu_rows<T, 64>(a, dma, s);
+        return with_tile(dtype, a.K, dma, false, a.M, 2 * (int64_t)a.F, 1, cdiv(a.K, Elem<T>::SLICE), [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.F, Tl::BN / 2);
             hipLaunchKernelGGL((k_glu_fwd<T, Tl>), dim3((unsigned)((int64_t)tm * tn)), dim3(Tl::NT), 0, s, a, tm,
@@ -278,7 +360,7 @@ hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s) {
 }
 
 int check_glu_prod(const GluProdArgs& a) {
-    const int64_t x = cdiv(a.M, 128) * cdiv(a.K, 128), w = cdiv(a.F, 128) * cdiv(a.K, 128);
+    const int64_t x = cdiv(a.M, 64) * cdiv(a.K, 64), w = cdiv(a.F, 64) * cdiv(a.K, 64);
     return x <= max_workgroups(512) && w <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
@@ -288,34 +370,44 @@ static hipError_t with_half(int dtype, Fn&& f) {
     return f(TypeTag<f16>{});
 }
 
+template <class T>
+static hipError_t launch_sum(const GluProdArgs& a, int64_t rows, unsigned copies, int n, hipStream_t s) {
+    hipLaunchKernelGGL((k_glu_sum<T>), dim3((unsigned)cdiv(rows * a.K, 256), copies), dim3(256), 0, s, a, (int)rows, n);
+    return hipGetLastError();
+}
+
 hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s) {
     // One tile's lines: 256 rows of dG, or a slice's 64 of W.
     const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 256) && dma_ok(dtype, a.W[0], a.ldw[0], a.K, 64) &&
                      dma_ok(dtype, a.W[1], a.ldw[1], a.K, 64) && a.ldw[0] == a.ldw[1];
+    const int n = dx_parts(a.M, a.F, a.K);
     return with_half(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        return with_tile(dtype, a.K, dma, a.M, a.K, 1, [&](auto tile) {
+        const hipError_t e = with_tile(dtype, a.K, dma, n > 1, a.M, a.K, 1, 2 * cdiv(a.F, 64), [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.K, Tl::BN);
-            hipLaunchKernelGGL((k_glu_dx<T, Tl>), dim3((unsigned)((int64_t)tm * tn)), dim3(Tl::NT), 0, s, a, tm,
-                               tn, xcd_remap_enabled());
+            hipLaunchKernelGGL((k_glu_dx<T, Tl>), dim3((unsigned)((int64_t)tm * tn), 1, (unsigned)n), dim3(Tl::NT),
+                               0, s, a, tm, tn, xcd_remap_enabled());
             return hipGetLastError();
         });
+        return e != hipSuccess || n == 1 ? e : launch_sum<T>(a, a.M, 1, n, s);
     });
 }
 
 hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s) {
     const unsigned both = a.C[0] != nullptr && a.C[1] != nullptr ? 2 : 1;
     const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 64) && dma_ok(dtype, a.X, a.ldx, a.K, 64);
+    const int n = dw_parts(a.M, a.F, a.K, (int)both);
     return with_half(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        return with_tile(dtype, a.K, dma, a.F, a.K, both, [&](auto tile) {
+        const hipError_t e = with_tile(dtype, a.K, dma, n > 1, a.F, a.K, both, cdiv(a.M, 64), [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.F, Tl::BM), tn = (int)cdiv(a.K, Tl::BN);
-            hipLaunchKernelGGL((k_glu_dw<T, Tl>), dim3((unsigned)((int64_t)tm * tn), both), dim3(Tl::NT), 0, s, a,
-                               tm, tn, xcd_remap_enabled());
+            hipLaunchKernelGGL((k_glu_dw<T, Tl>), dim3((unsigned)((int64_t)tm * tn), both, (unsigned)n),
+                               dim3(Tl::NT), 0, s, a, tm, tn, xcd_remap_enabled());
             return hipGetLastError();
         });
+        return e != hipSuccess || n == 1 ? e : launch_sum<T>(a, a.F, both, n, s);
     });
 }
 

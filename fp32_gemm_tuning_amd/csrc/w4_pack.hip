@@ -76,25 +76,36 @@ __global__ __launch_bounds__(256) void k_w4_quantize(PackArgs a) {
     }
 }
 
-// Two weights (one byte) per thread.
+// Eight weights (four bytes) a thread, all of one group. Bound by the bytes
+// written.
 template <class T>
 __global__ __launch_bounds__(256) void k_w4_dequantize(PackArgs a) {
-    const int bytes = (a.K + 1) / 2;
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    typedef T8 T8u __attribute__((aligned(sizeof(T))));
+    typedef uint32_t u32_u1 __attribute__((aligned(1)));
+    const int words = (a.K + 7) / 8;
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = at / bytes;
-    const int b = (int)(at - row * bytes);
+    const int64_t row = at / words;
+    const int k = (int)(at - row * words) * 8;
     if (row >= a.F) return;
-    const uint32_t q = a.Q[row * a.ldq + b];
-    const int g = 2 * b / a.group;
+    const uint8_t* q = a.Q + row * a.ldq + (k >> 1);
+    const int g = k / a.group;
     const float s = (float)((const T*)a.S)[row * a.lds + g];
     const float z = a.Z != nullptr ? (float)((const T*)a.Z)[row * a.ldz + g] : 8.0f;
-    T* w = const_cast<T*>((const T*)a.W) + row * a.ldw;
-    w[2 * b] = (T)(((float)(q & 15) - z) * s);
-    if (2 * b + 1 < a.K) w[2 * b + 1] = (T)(((float)(q >> 4) - z) * s);
+    T* w = const_cast<T*>((const T*)a.W) + row * a.ldw + k;
+    if (k + 8 <= a.K) {
+        const uint32_t v = *(const u32_u1*)q;
+        T8 x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (T)(((float)((v >> (4 * e)) & 15) - z) * s);
+        *(T8u*)w = x;
+    } else {
+        for (int e = 0; k + e < a.K; ++e) w[e] = (T)(((float)((q[e >> 1] >> (4 * (e & 1))) & 15) - z) * s);
+    }
 }
 
 static int64_t quantize_wgs(const PackArgs& a) { return cdiv((int64_t)a.F * cdiv(a.K, a.group), 4); }
-static int64_t dequantize_wgs(const PackArgs& a) { return cdiv((int64_t)a.F * cdiv(a.K, 2), 256); }
+static int64_t dequantize_wgs(const PackArgs& a) { return cdiv((int64_t)a.F * cdiv(a.K, 8), 256); }
 
 int check_w4_pack(const PackArgs& a) {
     return quantize_wgs(a) <= max_workgroups(256) && dequantize_wgs(a) <= max_workgroups(256)
