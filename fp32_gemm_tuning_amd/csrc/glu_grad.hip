@@ -39,8 +39,8 @@ __global__ __launch_bounds__(256) void k_glu_grad(GluGradArgs a) {
     for (int e = 0; e < 4; ++e) {
         if (col + e >= a.F) break;
         const float d = (float)dh[e];
-        du[e] = (T)(d * act_value(a.act, g[e]));
-        dg[e] = (T)(d * u[e] * act_slope(a.act, g[e]));
+        du[e] = (T)(d * act_value<sizeof(T) == 4>(a.act, g[e]));
+        dg[e] = (T)(d * u[e] * act_slope<sizeof(T) == 4>(a.act, g[e]));
     }
     *(T4*)((T*)a.dG + at) = dg;
     *(T4*)((T*)a.dU + at) = du;

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_fwd(GluArgs a, int tiles_m, int 
         const int row = m0 + i, f = f0 + (j >> 6) * 32 + (j & 31);
         if (row >= a.M || f >= a.F) return;
         const float g = acc[bi][bj][r], u = acc[bi][bj + 1][r];
-        ((T*)a.H)[(int64_t)row * a.ldh + f] = (T)(act_value(a.act, g) * u);
+        ((T*)a.H)[(int64_t)row * a.ldh + f] = (T)(act_value<sizeof(T) == 4>(a.act, g) * u);
         if (a.P != nullptr) {
             a.P[(int64_t)row * a.ldp + f] = g;
             a.P[(int64_t)row * a.ldp + a.F + f] = u;
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(KW * 64) void k_glu_rows(GluArgs a) {
         }
         const int row = m0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), f = f0 + (lane & 31);
         if (row >= a.M || f >= a.F) continue;
-        ((T*)a.H)[(int64_t)row * a.ldh + f] = (T)(act_value(a.act, g) * u);
+        ((T*)a.H)[(int64_t)row * a.ldh + f] = (T)(act_value<sizeof(T) == 4>(a.act, g) * u);
         if (a.P != nullptr) {
             a.P[(int64_t)row * a.ldp + f] = g;
             a.P[(int64_t)row * a.ldp + a.F + f] = u;

@@ -356,7 +356,7 @@ __global__ __launch_bounds__(512) void k_w4_few(W4Args a, W4Groups gr, int kw) {
         for (int d = 0; d < D; ++d)
             for (int i = 0; i < kw; ++i) v[d] += red[st * kw + i][(d * RW + r) * MR + m];
         if (m < a.M && f < a.F)
-            ((T*)a.Y)[(int64_t)m * a.ldy + f] = (T)(DUAL ? act_value(a.act, v[0]) * v[1] : v[0]);
+            ((T*)a.Y)[(int64_t)m * a.ldy + f] = (T)(DUAL ? act_value<sizeof(T) == 4>(a.act, v[0]) * v[1] : v[0]);
     }
 }
 
@@ -574,7 +574,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
             }
         const int m = m0 + 16 * i + row;
         if (m < a.M && f0 + f < a.F)
-            ((T*)a.Y)[(int64_t)m * a.ldy + f0 + f] = (T)(DUAL ? act_value(a.act, v[0]) * v[1] : v[0]);
+            ((T*)a.Y)[(int64_t)m * a.ldy + f0 + f] = (T)(DUAL ? act_value<sizeof(T) == 4>(a.act, v[0]) * v[1] : v[0]);
     }
 }
 

@@ -20,7 +20,89 @@ __device__ __forceinline__ uint32_t quantise(float w, float s, float inv, float 
     return (uint32_t)(int)n;
 }
 
-// One wave per group of one row.
+// A group's scale and zero point, and what its numbers are made with.
+template <class T>
+struct GroupForm {
+    T scale;
+    float s, inv, z;
+    bool flat, far;
+
+    // lo <= 0 and hi >= 0 are the group's extremes; `bad` is not 0 if it holds
+    // an infinity or NaN.
+    __device__ __forceinline__ GroupForm(float lo, float hi, float bad, bool asym) {
+        const double exact = asym ? ((double)hi - (double)lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
+        scale = bad == 0.0f ? (T)(float)exact : (T)__builtin_nanf("");
+        s = (float)scale;
+        z = 8.0f;
+        if (asym) z = s > 0.0f ? fminf((float)rint(-(double)lo / (double)s), 15.0f) : 0.0f;
+        flat = !(s > 0.0f);   // no scale (0 or NaN): every number is the zero point
+        inv = flat ? 0.0f : 1.0f / s;
+        far = !(inv <= 3.0e38f);   // 1 / s overflows: only the 64-bit quotient serves
+    }
+    __device__ __forceinline__ uint32_t number(float x) const {
+        if (flat) return (uint32_t)(int)z;
+        if (far) return (uint32_t)(int)fmin(fmax(rint((double)x / (double)s) + z, 0.0), 15.0);
+        return quantise(x, s, inv, z);
+    }
+};
+
+// Groups of 32 to 512 weights, a power of two: eight weights a lane, so a wave
+// takes 512 consecutive weights of a row and each group's extremes
+// are reduced over its LANES = group / 8 lanes. W is read once; bound by that.
+template <class T, int LANES>
+__global__ __launch_bounds__(256) void k_w4_quantize_row(PackArgs a) {
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    typedef T8 T8u __attribute__((aligned(sizeof(T))));
+    typedef uint32_t u32_u1 __attribute__((aligned(1)));
+    const int chunks = (a.K + 511) / 512;
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int64_t row = at / chunks;
+    const int k = (int)(at - row * chunks) * 512 + 8 * lane;
+    if (row >= a.F) return;
+    const T* w = (const T*)a.W + row * a.ldw + k;
+    float x[8];
+    if (k + 8 <= a.K) {
+        const T8 v = *(const T8u*)w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)v[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = k + e < a.K ? (float)w[e] : 0.0f;
+    }
+    float lo = 0.0f, hi = 0.0f, bad = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lo = fminf(lo, x[e]);
+        hi = fmaxf(hi, x[e]);
+        bad += x[e] - x[e];   // 0, or NaN for an infinity or NaN
+    }
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) {
+        lo = fminf(lo, __shfl_xor(lo, off));
+        hi = fmaxf(hi, __shfl_xor(hi, off));
+        bad += __shfl_xor(bad, off);
+    }
+    if (k >= a.K) return;
+    const bool asym = a.Z != nullptr;
+    const GroupForm<T> form(lo, hi, bad, asym);
+    if (lane % LANES == 0) {
+        const int g = k / (8 * LANES);
+        ((T*)a.S)[row * a.lds + g] = form.scale;
+        if (asym) ((T*)a.Z)[row * a.ldz + g] = (T)form.z;
+    }
+    uint32_t v = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v |= (k + e < a.K ? form.number(x[e]) : 0u) << (4 * e);
+    uint8_t* q = a.Q + row * a.ldq + (k >> 1);
+    if (k + 8 <= a.K) {
+        *(u32_u1*)q = v;
+    } else {
+        for (int e = 0; k + e < a.K; e += 2) q[e >> 1] = (uint8_t)(v >> (4 * e));
+    }
+}
+
+// Any other group: one wave each, W read twice.
 template <class T>
 __global__ __launch_bounds__(256) void k_w4_quantize(PackArgs a) {
     const int groups = (a.K + a.group - 1) / a.group;
@@ -36,7 +118,7 @@ __global__ __launch_bounds__(256) void k_w4_quantize(PackArgs a) {
         const float x = (float)w[k];
         lo = fminf(lo, x);
         hi = fmaxf(hi, x);
-        bad += x - x;   // 0, or NaN for an infinity or NaN
+        bad += x - x;
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
@@ -45,34 +127,16 @@ __global__ __launch_bounds__(256) void k_w4_quantize(PackArgs a) {
         bad += __shfl_xor(bad, off);
     }
     const bool asym = a.Z != nullptr;
-    const double exact = asym ? ((double)hi - (double)lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
-    const T st = bad == 0.0f ? (T)(float)exact : (T)__builtin_nanf("");
-    const float s = (float)st;
-    float z = 8.0f;
-    if (asym) z = s > 0.0f ? fminf((float)rint(-(double)lo / (double)s), 15.0f) : 0.0f;
+    const GroupForm<T> form(lo, hi, bad, asym);
     if (lane == 0) {
-        ((T*)a.S)[row * a.lds + g] = st;
-        if (asym) ((T*)a.Z)[row * a.ldz + g] = (T)z;
+        ((T*)a.S)[row * a.lds + g] = form.scale;
+        if (asym) ((T*)a.Z)[row * a.ldz + g] = (T)form.z;
     }
-    // No scale (0 or NaN): every number is the zero point.
-    const bool flat = !(s > 0.0f);
-    const float inv = flat ? 0.0f : 1.0f / s;
-    const bool far = !(inv <= 3.0e38f);   // 1 / s overflows: only the 64-bit quotient serves
     uint8_t* q = a.Q + row * a.ldq;
     for (int k = k0 + 2 * lane; k < k1; k += 128) {
-        uint32_t v[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (k + e >= a.K) break;
-            const float x = (float)w[k + e];
-            if (flat)
-                v[e] = (uint32_t)(int)z;
-            else if (far)
-                v[e] = (uint32_t)(int)fmin(fmax(rint((double)x / (double)s) + z, 0.0), 15.0);
-            else
-                v[e] = quantise(x, s, inv, z);
-        }
-        q[k >> 1] = (uint8_t)(v[0] | (v[1] << 4));
+        uint32_t v = form.number((float)w[k]);
+        if (k + 1 < a.K) v |= form.number((float)w[k + 1]) << 4;
+        q[k >> 1] = (uint8_t)v;
     }
 }
 
@@ -104,7 +168,12 @@ __global__ __launch_bounds__(256) void k_w4_dequantize(PackArgs a) {
     }
 }
 
-static int64_t quantize_wgs(const PackArgs& a) { return cdiv((int64_t)a.F * cdiv(a.K, a.group), 4); }
+// Whether k_w4_quantize_row takes the call's groups (a group of at least K is one a row, so it may
+// be any multiple of 32).
+static bool by_row(const PackArgs& a) { return a.group <= 512 && (a.group & (a.group - 1)) == 0; }
+static int64_t quantize_wgs(const PackArgs& a) {
+    return cdiv((int64_t)a.F * (by_row(a) ? cdiv(a.K, 512) : cdiv(a.K, a.group)), 4);
+}
 static int64_t dequantize_wgs(const PackArgs& a) { return cdiv((int64_t)a.F * cdiv(a.K, 8), 256); }
 
 int check_w4_pack(const PackArgs& a) {
@@ -115,7 +184,19 @@ int check_w4_pack(const PackArgs& a) {
 hipError_t launch_w4_quantize(int dtype, const PackArgs& a, hipStream_t s) {
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        hipLaunchKernelGGL((k_w4_quantize<T>), dim3((unsigned)quantize_wgs(a)), dim3(256), 0, s, a);
+        const dim3 grid((unsigned)quantize_wgs(a)), block(256);
+        if (!by_row(a))
+            hipLaunchKernelGGL((k_w4_quantize<T>), grid, block, 0, s, a);
+        else if (a.group == 32)
+            hipLaunchKernelGGL((k_w4_quantize_row<T, 4>), grid, block, 0, s, a);
+        else if (a.group == 64)
+            hipLaunchKernelGGL((k_w4_quantize_row<T, 8>), grid, block, 0, s, a);
+        else if (a.group == 128)
+            hipLaunchKernelGGL((k_w4_quantize_row<T, 16>), grid, block, 0, s, a);
+        else if (a.group == 256)
+            hipLaunchKernelGGL((k_w4_quantize_row<T, 32>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((k_w4_quantize_row<T, 64>), grid, block, 0, s, a);
         return hipGetLastError();
     });
 }

@@ -262,7 +262,7 @@ def test_empty_sums(dev):
 # ---------------------------------------------------------------------------
 # (F, K, group)
 PACKS = [(1, 1, 32), (3, 31, 32), (5, 33, 32), (7, 777, 64), (64, 256, 128), (33, 100, 1000), (16, 130, 96),
-         (20, 519, 256)]
+         (20, 519, 256), (6, 1300, 512), (5, 1100, 1024)]
 
 
 @pytest.mark.parametrize("zeros", [False, True], ids=["symmetric", "zeros"])
