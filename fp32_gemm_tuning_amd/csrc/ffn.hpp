@@ -107,7 +107,7 @@ struct GluGradArgs {
     int32_t act;
 };
 
-// A 16-bit product of the backward pass. dX: C0 = dG W[0] + dU W[1]; dW:
+// A product of the backward pass. dX: C0 = dG W[0] + dU W[1]; dW:
 // C0 = dG^T X, C1 = dU^T X (either may be null). D are dG and dU (M x F,
 // leading dimension ldd); part is the space of split products' partial sums
 // (glu_prod_bytes).
@@ -148,7 +148,11 @@ struct PackArgs {
 int check_glu(const GluArgs& a);
 hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s);
 int check_glu_prod(const GluProdArgs& a);
-size_t glu_prod_bytes(int64_t M, int64_t F, int64_t K);
+// Whether the backward products of these sizes run on launch_glu_dx and
+// launch_glu_dw (16-bit ones do) or, FP32, on sgemm_f32_ws.
+bool glu_dx_here(int dtype, int64_t M, int64_t K);
+bool glu_dw_here(int dtype, int64_t F, int64_t K);
+size_t glu_prod_bytes(int dtype, int64_t M, int64_t F, int64_t K);
 hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s);
 hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s);
 // glu_grad.hip

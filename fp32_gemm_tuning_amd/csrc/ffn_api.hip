@@ -41,8 +41,8 @@ int32_t group_of(int64_t group, int64_t K) {
 
 // The backward pass's workspace: dG and dU, each M rows of ldd elements (F
 // rounded up to whole 64-element slices, so that their rows are whole 16-byte
-// chunks), then, for FP32, what the stream-K kernels of its products may use, or
-// the partial sums of 16-bit products that are split.
+// chunks), then the partial sums of products that are split, or, for large
+// FP32 products, what the stream-K kernels may use.
 struct BwdSpace {
     int64_t ldd;
     size_t du_at, sk_at, sk_bytes, total;
@@ -52,7 +52,7 @@ int bwd_space(int dtype, int64_t M, int64_t F, int64_t K, int num_cus, BwdSpace*
     const size_t one = up256((size_t)M * (size_t)o->ldd * (size_t)dtype_bytes(dtype));
     o->du_at = one;
     o->sk_at = 2 * one;
-    o->sk_bytes = 0;
+    size_t most = glu_prod_bytes(dtype, M, F, K);
     if (dtype == SGEMM_F32_DTYPE_F32) {
         size_t dx = 0, dw = 0;
         int rc = sgemm_f32_ws_size(-1, SGEMM_F32_ROW_MAJOR, SGEMM_F32_NO_TRANS, SGEMM_F32_NO_TRANS, M, K,
@@ -61,10 +61,10 @@ int bwd_space(int dtype, int64_t M, int64_t F, int64_t K, int num_cus, BwdSpace*
             rc = sgemm_f32_ws_size(-1, SGEMM_F32_ROW_MAJOR, SGEMM_F32_TRANS, SGEMM_F32_NO_TRANS, F, K, M,
                                    num_cus, &dw);
         if (rc) return rc;
-        o->sk_bytes = up256(dx > dw ? dx : dw);
-    } else {
-        o->sk_bytes = up256(glu_prod_bytes(M, F, K));
+        most = dx > most ? dx : most;
+        most = dw > most ? dw : most;
     }
+    o->sk_bytes = up256(most);
     o->total = o->sk_at + o->sk_bytes;
     return 0;
 }
@@ -208,45 +208,43 @@ SGEMM_F32_API int sgemm_f32_glu_bwd(int dtype, int act, int64_t M, int64_t F, in
                      {0, 0}, (int32_t)M, (int32_t)F, (int32_t)K};
     const GluGradArgs g = {P, dH, ws, ws + sp.du_at, ldp, lddh, sp.ldd, (int32_t)M, (int32_t)F, act};
     rc = check_glu_grad(g);
-    if (rc == 0 && dtype != SGEMM_F32_DTYPE_F32) rc = check_glu_prod(p);
+    if (rc == 0) rc = check_glu_prod(p);
     if (rc) return rc;
     if (grads) {
         rc = status(launch_glu_grad(dtype, g, s));
         if (rc) return rc;
     }
-    if (dtype == SGEMM_F32_DTYPE_F32) {
-        const float* dg = (const float*)p.D[0];
-        const float* du = (const float*)p.D[1];
-        void* sk = ws + sp.sk_at;
-        const int R = SGEMM_F32_ROW_MAJOR, N = SGEMM_F32_NO_TRANS, T = SGEMM_F32_TRANS;
-        if (want_x) {
+    const float* dg = (const float*)p.D[0];
+    const float* du = (const float*)p.D[1];
+    void* sk = ws + sp.sk_at;
+    const int R = SGEMM_F32_ROW_MAJOR, N = SGEMM_F32_NO_TRANS, T = SGEMM_F32_TRANS;
+    if (want_x) {
+        if (glu_dx_here(dtype, M, K)) {
+            p.C[0] = dX;
+            p.ldc[0] = lddx;
+            rc = status(launch_glu_dx(dtype, p, s));
+        } else {
             rc = sgemm_f32_ws(R, N, N, M, K, F, 1.0f, dg, sp.ldd, (const float*)Wg, ldwg, 0.0f, (float*)dX,
                               lddx, sk, sp.sk_bytes, stream);
             if (rc == 0)
                 rc = sgemm_f32_ws(R, N, N, M, K, F, 1.0f, du, sp.ldd, (const float*)Wu, ldwu, 1.0f,
                                   (float*)dX, lddx, sk, sp.sk_bytes, stream);
         }
-        if (rc == 0 && want_g)
-            rc = sgemm_f32_ws(R, T, N, F, K, M, 1.0f, dg, sp.ldd, (const float*)X, ldx, 0.0f, (float*)dWg,
-                              lddwg, sk, sp.sk_bytes, stream);
-        if (rc == 0 && want_u)
-            rc = sgemm_f32_ws(R, T, N, F, K, M, 1.0f, du, sp.ldd, (const float*)X, ldx, 0.0f, (float*)dWu,
-                              lddwu, sk, sp.sk_bytes, stream);
-        return rc;
-    }
-    if (want_x) {
-        p.C[0] = dX;
-        p.ldc[0] = lddx;
-        rc = status(launch_glu_dx(dtype, p, s));
         if (rc) return rc;
     }
-    if (want_g || want_u) {
+    if ((want_g || want_u) && glu_dw_here(dtype, F, K)) {
         p.C[0] = want_g ? dWg : nullptr;
         p.C[1] = want_u ? dWu : nullptr;
         p.ldc[0] = lddwg;
         p.ldc[1] = lddwu;
-        rc = status(launch_glu_dw(dtype, p, s));
+        return status(launch_glu_dw(dtype, p, s));
     }
+    if (want_g)
+        rc = sgemm_f32_ws(R, T, N, F, K, M, 1.0f, dg, sp.ldd, (const float*)X, ldx, 0.0f, (float*)dWg, lddwg,
+                          sk, sp.sk_bytes, stream);
+    if (rc == 0 && want_u)
+        rc = sgemm_f32_ws(R, T, N, F, K, M, 1.0f, du, sp.ldd, (const float*)X, ldx, 0.0f, (float*)dWu, lddwu,
+                          sk, sp.sk_bytes, stream);
     return rc;
 }
 

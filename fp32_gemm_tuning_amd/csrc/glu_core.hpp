@@ -105,8 +105,11 @@ __device__ __forceinline__ i32x4 place_chunk(const i32x4& v, const Lines<T>& s, 
 // LDS placement of an RC operand's 16-byte chunk (k line, chunk of 8 rows):
 // the four k lines that one transposed read takes (kline & 3) lie in distinct
 // 64-byte quarters of the 256 bytes that the banks span.
-template <int ROWS>
+// FP32 fragments are read as single words, a row's four k from four lines, and
+// need no placement.
+template <class T, int ROWS>
 __device__ __forceinline__ int rc_chunk(int kline, int c) {
+    if (sizeof(T) == 4) return c;
     return c ^ (ROWS >= 128 ? (kline & 3) << 2 : ((kline >> 1) & 1) << 2);
 }
 
@@ -159,7 +162,7 @@ struct RegFill {
             int at;
             if constexpr (RC) {
                 const int k = slot / CPL;
-                at = k * CPL + rc_chunk<ROWS>(k, slot % CPL);
+                at = k * CPL + rc_chunk<T, ROWS>(k, slot % CPL);
             } else {
                 const int row = slot / 8;
                 at = row * 8 + ((slot % 8) ^ swz_chunk<32>(row));
@@ -180,12 +183,15 @@ struct RegFill {
 template <class T, int ROWS, bool RC>
 __device__ __forceinline__ i32x4 read_frag(const char* lds, int row0, int lane, int v) {
     const int h = lane >> 5;
-    if constexpr (RC) {
+    if constexpr (RC && sizeof(T) == 4) {
+        const int* p = (const int*)lds + (16 * h + 4 * v) * ROWS + row0 + (lane & 31);
+        return i32x4{p[0], p[ROWS], p[2 * ROWS], p[3 * ROWS]};
+    } else if constexpr (RC) {
         const int i = lane & 15, row = row0 + (lane & 16) + 4 * (i & 3);
         const int k = 32 * h + 8 * v + (i >> 2);
         constexpr int PITCH = ROWS * 2;
-        const char* lo = lds + k * PITCH + rc_chunk<ROWS>(k, row >> 3) * 16 + (row & 7) * 2;
-        const char* hi = lds + (k + 4) * PITCH + rc_chunk<ROWS>(k + 4, row >> 3) * 16 + (row & 7) * 2;
+        const char* lo = lds + k * PITCH + rc_chunk<T, ROWS>(k, row >> 3) * 16 + (row & 7) * 2;
+        const char* hi = lds + (k + 4) * PITCH + rc_chunk<T, ROWS>(k + 4, row >> 3) * 16 + (row & 7) * 2;
         return read_tr(lo, hi);
     } else {
         const int row = row0 + (lane & 31);
@@ -199,18 +205,77 @@ __device__ __forceinline__ i32x4 read_frag(const char* lds, int row0, int lane, 
 // register sets keep the loads of the next two slices in flight (a slice's
 // products are shorter than a load's way from memory), and the barrier waits for
 // LDS only.
-template <class T, int BM, int BN, int WM, int WN, bool ARC, bool BRC, bool PAIR, bool SHORT = false>
+//
+// KS = 2: two waves share each wave tile and take half of every slice each, so that
+// a small tile has four waves; exchange() adds their sums, each wave then
+// holding half of the rows of each block (registers 0 .. 7).
+template <int BM, int BN, int WM, int WN, int KS>
+struct WaveMap {
+    static constexpr int WAVES_N = BN / WN, WAVES = (BM / WM) * WAVES_N;
+    static constexpr int BI = WM / 32, BJ = WN / 32, REGS = 16 / KS;
+    int wm, wn, kk, lane, w;
+    __device__ __forceinline__ WaveMap() {
+        const int t = threadIdx.x;
+        lane = t & 63;
+        w = t >> 6;
+        kk = KS == 1 ? 0 : w / WAVES;
+        const int mn = KS == 1 ? w : w - kk * WAVES;
+        wm = (mn / WAVES_N) * WM;
+        wn = (mn % WAVES_N) * WN;
+    }
+    // `space`: 64 lanes x BI BJ 16 words for each wave, free to be written.
+    __device__ __forceinline__ void exchange(float* const* space, f32x16 (&acc)[BI][BJ]) const {
+        if constexpr (KS > 1) {
+#pragma unroll
+            for (int i = 0; i < BI; ++i)
+#pragma unroll
+                for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) space[w][((i * BJ + j) * 16 + r) * 64 + lane] = acc[i][j][r];
+            __syncthreads();
+            const int mn = w - kk * WAVES;
+#pragma unroll
+            for (int i = 0; i < BI; ++i)
+#pragma unroll
+                for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < REGS; ++r) {
+                        float v = 0.0f;
+#pragma unroll
+                        for (int g = 0; g < KS; ++g)
+                            v += space[mn + g * WAVES][((i * BJ + j) * 16 + kk * REGS + r) * 64 + lane];
+                        acc[i][j][r] = v;
+                    }
+        }
+    }
+    // f(block row, block column, register, tile row, tile column) of this wave's results.
+    template <class Fn>
+    __device__ __forceinline__ void each(Fn&& f) const {
+#pragma unroll
+        for (int bi = 0; bi < BI; ++bi)
+#pragma unroll
+            for (int bj = 0; bj < BJ; ++bj)
+#pragma unroll
+                for (int r = 0; r < REGS; ++r) {
+                    const int rr = kk * REGS + r;
+                    f(bi, bj, r, wm + 32 * bi + 8 * (rr >> 2) + 4 * (lane >> 5) + (rr & 3),
+                      wn + 32 * bj + (lane & 31));
+                }
+    }
+};
+
+template <class T, int BM, int BN, int WM, int WN, bool ARC, bool BRC, bool PAIR, int KS = 1, bool SHORT = false>
 struct TileCore {
-    static constexpr int WAVES_N = BN / WN;
-    static constexpr int NT = (BM / WM) * WAVES_N * 64;
+    using Map = WaveMap<BM, BN, WM, WN, KS>;
+    static constexpr int NT = Map::WAVES * KS * 64;
     static constexpr int BI = WM / 32, BJ = WN / 32;
     static constexpr int STAGE = (BM + BN) * 128;
 
     template <class Src>
     __device__ __forceinline__ static void run(char* lds, int m0, int n0, int s_begin, int s_end, Src&& src,
                                                f32x16 (&acc)[BI][BJ]) {
-        const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-        const int wm = (w / WAVES_N) * WM, wn = (w % WAVES_N) * WN;
+        const Map map;
+        const int t = threadIdx.x, lane = map.lane, wm = map.wm, wn = map.wn;
 #pragma unroll
         for (int i = 0; i < BI; ++i)
 #pragma unroll
@@ -238,7 +303,8 @@ struct TileCore {
         auto compute = [&](const char* A) {
             const char* B = A + BM * 128;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
+            for (int p = 0; p < 4 / KS; ++p) {
+                const int v = map.kk * (4 / KS) + p;
                 i32x4 a[BI], b[BJ];
 #pragma unroll
                 for (int i = 0; i < BI; ++i) a[i] = read_frag<T, BM, ARC>(A, wm + 32 * i, lane, v);
@@ -269,22 +335,16 @@ struct TileCore {
             slice(s, lds, lds + STAGE, r1);
             slice(s + 1, lds + STAGE, lds, r0);
         }
-        if (s < s_end) compute(lds);
-    }
-
-    // f(i, j, register values of block (bi, bj) at tile row i, tile column j).
-    template <class Fn>
-    __device__ __forceinline__ static void each(Fn&& f) {
-        const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-        const int wm = (w / WAVES_N) * WM, wn = (w % WAVES_N) * WN;
-#pragma unroll
-        for (int bi = 0; bi < BI; ++bi)
-#pragma unroll
-            for (int bj = 0; bj < BJ; ++bj)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    f(bi, bj, r, wm + 32 * bi + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3),
-                      wn + 32 * bj + (lane & 31));
+        if (s < s_end) {
+            compute(lds);
+            ring_barrier<63>();
+        }
+        if constexpr (KS > 1) {
+            float* const space[4] = {(float*)lds, (float*)(lds + STAGE / 2), (float*)(lds + STAGE),
+                                     (float*)(lds + STAGE + STAGE / 2)};
+            static_assert(Map::WAVES * KS == 4 && BI * BJ * 16 * 64 * 4 <= STAGE / 2, "a wave's sums fit");
+            map.exchange(space, acc);
+        }
     }
 };
 
@@ -330,7 +390,7 @@ struct DmaFill {
             const int slot = (w + W * p) * 64 + lane;
             const int64_t ld = PAIR && matrix(w, p) ? s[1].ld : s[0].ld;
             if constexpr (RC) {
-                const int k = slot / CPL, c = rc_chunk<ROWS>(k, slot % CPL);
+                const int k = slot / CPL, c = rc_chunk<T, ROWS>(k, slot % CPL);
                 off[p] = r0 + c * EPC < extent ? (uint32_t)((k * (int)ld + c * EPC) * (int)sizeof(T)) : OOB;
             } else {
                 const int row = slot / 8, src = PAIR ? (row >> 6) * 32 + (row & 31) : row;
@@ -368,15 +428,14 @@ struct DmaFill {
     }
 };
 
-template <class T, int BM, int BN, int WM, int WN, bool ARC, bool BRC, bool PAIR>
+template <class T, int BM, int BN, int WM, int WN, bool ARC, bool BRC, bool PAIR, int KS = 1>
 struct DmaCore {
-    static constexpr int WAVES_N = BN / WN;
-    static constexpr int NT = (BM / WM) * WAVES_N * 64;
+    using Map = WaveMap<BM, BN, WM, WN, KS>;
+    static constexpr int NT = Map::WAVES * KS * 64;
     static constexpr int BI = WM / 32, BJ = WN / 32;
     static constexpr int LDS_A = BM * 128, LDS_B = BN * 128;
     using FA = DmaFill<T, BM, NT, ARC>;
     using FB = DmaFill<T, BN, NT, BRC>;
-    using Out = TileCore<T, BM, BN, WM, WN, ARC, BRC, PAIR>;   // for each()
 
     struct Frag {
         i32x4 a[BI], b[BJ];
@@ -388,7 +447,8 @@ struct DmaCore {
     __device__ __forceinline__ static void weave() {
         constexpr int MFMA = 0x008, VMEM_READ = 0x020, DS_READ = 0x100;
         constexpr int MFMAS = BI * BJ * (sizeof(T) == 4 ? 4 : 1);
-        constexpr int READS = BI * (ARC ? 2 : 1) + BJ * (BRC ? 2 : 1);
+        constexpr int RC_READS = sizeof(T) == 4 ? 4 : 2;
+        constexpr int READS = BI * (ARC ? RC_READS : 1) + BJ * (BRC ? RC_READS : 1);
         constexpr int RN = MFMAS > 2 ? MFMAS - 2 : 1, RS = (READS + RN - 1) / RN;   // reads after each of the first RN
         constexpr int LS = LOADS == 0 ? 1 : (LOADS + MFMAS - 2) / (MFMAS - 1);
 #pragma unroll
@@ -403,8 +463,8 @@ struct DmaCore {
     template <class Src>
     __device__ __forceinline__ static void run(char* a0, char* b0, char* a1, char* b1, int m0, int n0,
                                                int s_begin, int s_end, Src&& src, f32x16 (&acc)[BI][BJ]) {
-        const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-        const int wm = (w / WAVES_N) * WM, wn = (w % WAVES_N) * WN;
+        const Map map;
+        const int t = threadIdx.x, lane = map.lane, wm = map.wm, wn = map.wn;
 #pragma unroll
         for (int i = 0; i < BI; ++i)
 #pragma unroll
@@ -442,22 +502,19 @@ struct DmaCore {
         issue(s_begin, a0, b0);
         issue(s_begin + 1, a1, b1);   // past the last slice: never used
         ring_barrier<FA::G + FB::G>();
-        read(f0, a0, b0, 0);
+        constexpr int PARTS = 4 / KS;
+        const int v0 = map.kk * PARTS;
+        read(f0, a0, b0, v0);
         auto slice = [&](int s, char* A, char* B, char* An, char* Bn) {
-            read(f1, A, B, 1);
-            mma(f0);
-            weave<0>();
-            __builtin_amdgcn_sched_barrier(0);
-            read(f0, A, B, 2);
-            mma(f1);
-            weave<0>();
-            __builtin_amdgcn_sched_barrier(0);
-            read(f1, A, B, 3);
-            mma(f0);
-            weave<0>();
-            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int p = 0; p + 1 < PARTS; ++p) {
+                read(p & 1 ? f0 : f1, A, B, v0 + p + 1);
+                mma(p & 1 ? f1 : f0);
+                weave<0>();
+                __builtin_amdgcn_sched_barrier(0);
+            }
             ring_barrier<0>();
-            read(f0, An, Bn, 0);
+            read(f0, An, Bn, v0);
             mma(f1);
             issue(s + 2, A, B);
             weave<FA::G + FB::G>();
@@ -470,6 +527,12 @@ struct DmaCore {
         }
         if (s < s_end) slice(s, a0, b0, a1, b1);
         ring_barrier<0>();   // the loads past the last slice land before LDS is given up
+        if constexpr (KS > 1) {
+            float* const space[4] = {(float*)a0, (float*)b0, (float*)a1, (float*)b1};
+            static_assert(Map::WAVES * KS == 4 && BI * BJ * 16 * 64 * 4 <= (LDS_A < LDS_B ? LDS_A : LDS_B),
+                          "a wave's sums fit");
+            map.exchange(space, acc);
+        }
     }
 };
 

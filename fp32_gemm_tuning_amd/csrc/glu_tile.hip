@@ -26,13 +26,14 @@ __device__ __forceinline__ void product(int m0, int n0, int s_begin, int s_end, 
 
 // Block and wave tile, and how it is filled: buffer-to-LDS loads (DMA) or
 // through registers, element by element where rows are shorter than 16 bytes.
-template <int BM_, int BN_, int WM_, int WN_, bool DMA_, bool SHORT_ = false>
+template <int BM_, int BN_, int WM_, int WN_, int KS_, bool DMA_, bool SHORT_ = false>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NT = (BM / WM) * (BN / WN) * 64;
+    static constexpr int BM = BM_, BN = BN_, NT = (BM_ / WM_) * (BN_ / WN_) * KS_ * 64;
     static constexpr bool DMA = DMA_;
+    using Map = WaveMap<BM_, BN_, WM_, WN_, KS_>;
     template <class T, bool ARC, bool BRC, bool PAIR>
-    using Core = std::conditional_t<DMA_, DmaCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR>,
-                                    TileCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, SHORT_>>;
+    using Core = std::conditional_t<DMA_, DmaCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, KS_>,
+                                    TileCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, KS_, SHORT_>>;
 };
 
 // H = act(X Wg^T) * (X Wu^T). A tile's columns alternate between the two
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_fwd(GluArgs a, int tiles_m, int 
         return s * Elem<T>::SLICE;
     };
     product<Core, Tl::DMA>(m0, f0, 0, (a.K + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
-    TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, false, false, true>::each([&](int bi, int bj, int r, int i, int j) {
+    typename Tl::Map().each([&](int bi, int bj, int r, int i, int j) {
         if (bj & 1) return;
         const int row = m0 + i, f = f0 + (j >> 6) * 32 + (j & 31);
         if (row >= a.M || f >= a.F) return;
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, i
         return (s - u * half) * Elem<T>::SLICE;
     };
     product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
-    TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, false, true, false>::each([&](int bi, int bj, int r, int i, int j) {
+    typename Tl::Map().each([&](int bi, int bj, int r, int i, int j) {
         const int row = m0 + i, col = n0 + j;
         if (row < a.M && col < a.K) put<T>(a, 0, a.M, row, col, acc[bi][bj][r]);
     });
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dw(GluProdArgs a, int tiles_m, i
         return s * Elem<T>::SLICE;
     };
     product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
-    TileCore<T, Tl::BM, Tl::BN, Tl::WM, Tl::WN, true, true, false>::each([&](int bi, int bj, int r, int i, int j) {
+    typename Tl::Map().each([&](int bi, int bj, int r, int i, int j) {
         const int f = m0 + i, col = n0 + j;
         if (f < a.F && col < a.K) put<T>(a, u, a.F, f, col, acc[bi][bj][r]);
     });
@@ -249,12 +250,12 @@ __global__ __launch_bounds__(256) void k_glu_sum(GluProdArgs a, int rows, int pa
     ((T*)(u ? a.C[1] : a.C[0]))[row * (u ? a.ldc[1] : a.ldc[0]) + (at - row * a.K)] = (T)v;
 }
 
-using TileReg = Tile<128, 128, 64, 64, false>;
-using TileReg64 = Tile<64, 64, 32, 64, false>;
-using TileDma64 = Tile<64, 64, 32, 64, true>;
-using TileShort = Tile<128, 128, 64, 64, false, true>;
-using TileMid = Tile<128, 128, 64, 64, true>;
-using TileBig = Tile<256, 256, 128, 64, true>;
+using TileReg = Tile<128, 128, 64, 64, 1, false>;
+using TileReg64 = Tile<64, 64, 32, 64, 2, false>;
+using TileDma64 = Tile<64, 64, 32, 64, 2, true>;
+using TileShort = Tile<128, 128, 64, 64, 1, false, true>;
+using TileMid = Tile<128, 128, 64, 64, 1, true>;
+using TileBig = Tile<256, 256, 128, 64, 1, true>;
 
 // Whether an operand of `lines` lines can be filled by buffer-to-LDS loads:
 // whole 16-byte chunks, and a tile's span within 31-bit byte offsets.
@@ -265,11 +266,11 @@ static bool dma_ok(int dtype, const void* p, int64_t ld, int64_t extent, int64_t
 }
 
 // Times that the choice of a tile goes by, in microseconds, measured on MI355X
-// (products of 512 x 2048 x 2048 to 4096 x 8192 x 4096): a call takes about
+// (products of 300 x 1000 x 511 to 4096 x 8192 x 4096): a call takes about
 //     fixed + n max(alone, tiles per compute unit * busy)
 // for n slices, with `alone` a slice of a lone tile and `busy` a slice's share of a
 // unit that holds several. FP32 slices hold half the k and take the matrix
-// cores eight times as long.
+// cores eight times as long; register-filled tiles wait longer per slice.
 struct TileCost {
     double fixed, alone, busy;
     double of(int64_t tiles, int64_t slices) const {
@@ -277,26 +278,32 @@ struct TileCost {
         return fixed + (double)slices * (b > alone ? b : alone);
     }
 };
+// [FP32][filled through registers]
 static const TileCost kBig[2] = {{9.0, 1.8, 1.8}, {9.0, 7.3, 7.3}};
-static const TileCost kMid[2] = {{7.0, 0.45, 0.52}, {7.0, 2.2, 2.0}};
-static const TileCost k64[2] = {{6.0, 0.28, 0.19}, {6.0, 0.70, 0.66}};
+static const TileCost kMid[2][2] = {{{7.0, 0.45, 0.52}, {7.0, 1.1, 0.85}}, {{7.0, 2.2, 2.0}, {7.0, 2.8, 2.2}}};
+static const TileCost k64[2][2] = {{{6.0, 0.25, 0.19}, {6.0, 0.50, 0.30}}, {{6.0, 0.60, 0.60}, {6.0, 0.80, 0.73}}};
 
 // f(tile tag): the tile that the model above finds fastest; filled through registers
 // where an operand is not whole chunks (never the big tile: its registers
-// are taken). `split`: the product is split, which the 64 x 64 tiles do.
-template <class Fn>
-static hipError_t with_tile(int dtype, int K, bool dma, bool split, int64_t rows, int64_t cols, int64_t copies,
-                            int64_t slices, Fn&& f) {
-    const int f32 = dtype == SGEMM_F32_DTYPE_F32;
+// are taken). SMALL: a product that is split, or an FP32 one, which only the
+// 64 x 64 tiles take.
+template <bool SMALL, class Fn>
+static hipError_t with_tile(int dtype, int K, bool dma, int64_t rows, int64_t cols, int64_t copies, int64_t slices,
+                            Fn&& f) {
     if (K < 16 / dtype_bytes(dtype)) return f(TypeTag<TileShort>{});
-    auto tiles = [&](int64_t b) { return cdiv(rows, b) * cdiv(cols, b) * copies; };
-    const double c64 = k64[f32].of(tiles(64), slices), cmid = kMid[f32].of(tiles(128), slices);
-    const double cbig = kBig[f32].of(tiles(256), slices);
-    if (split || (c64 < cmid && (!dma || c64 < cbig)))
-        return dma ? f(TypeTag<TileDma64>{}) : f(TypeTag<TileReg64>{});
-    if (!dma) return f(TypeTag<TileReg>{});
-    if (cbig < cmid) return f(TypeTag<TileBig>{});
-    return f(TypeTag<TileMid>{});
+    if constexpr (!SMALL) {
+        const int f32 = dtype == SGEMM_F32_DTYPE_F32;
+        auto tiles = [&](int64_t b) { return cdiv(rows, b) * cdiv(cols, b) * copies; };
+        const double small = k64[f32][!dma].of(tiles(64), slices), mid = kMid[f32][!dma].of(tiles(128), slices);
+        if (dma) {
+            const double big = kBig[f32].of(tiles(256), slices);
+            if (big < mid && big < small) return f(TypeTag<TileBig>{});
+            if (mid < small) return f(TypeTag<TileMid>{});
+        } else if (mid < small) {
+            return f(TypeTag<TileReg>{});
+        }
+    }
+    return dma ? f(TypeTag<TileDma64>{}) : f(TypeTag<TileReg64>{});
 }
 
 // Parts that a product of few tiles is split into: as many as make 512 of the
@@ -308,17 +315,30 @@ static int parts(int64_t rows, int64_t cols, int64_t copies, int64_t slices, int
     const int64_t by_tiles = 512 / tiles, by_slices = slices / 4, n = by_tiles < by_slices ? by_tiles : by_slices;
     return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
-static int dx_parts(int64_t M, int64_t F, int64_t K) { return parts(M, K, 1, 2 * cdiv(F, 64), (int)K); }
-static int dw_parts(int64_t M, int64_t F, int64_t K, int copies) { return parts(F, K, copies, cdiv(M, 64), (int)K); }
-size_t glu_prod_bytes(int64_t M, int64_t F, int64_t K) {
+static int64_t slice_of(int dtype) { return 128 / dtype_bytes(dtype); }
+static int dx_parts(int dtype, int64_t M, int64_t F, int64_t K) {
+    return parts(M, K, 1, 2 * cdiv(F, slice_of(dtype)), (int)K);
+}
+// (as for both gradients, so that one alone has the same bits)
+static int dw_parts(int dtype, int64_t M, int64_t F, int64_t K) {
+    return parts(F, K, 2, cdiv(M, slice_of(dtype)), (int)K);
+}
+// FP32 products up to 640 tiles run here, larger ones on the library's own dispatch
+// (tiles of 64 x 64: dX of 77 x 1000 x 511 16.4 us against 18.3, 1000 x 1531 x 777 83
+// against 89, dW of 4096 x 500 x 500 45 against 54; dX of 2000 x 2000 x 1500
+// 230 against 214).
+static bool here(int dtype, int64_t rows, int64_t cols, int64_t copies) {
+    return dtype != SGEMM_F32_DTYPE_F32 || cdiv(rows, 64) * cdiv(cols, 64) * copies <= 640;
+}
+bool glu_dx_here(int dtype, int64_t M, int64_t K) { return here(dtype, M, K, 1); }
+bool glu_dw_here(int dtype, int64_t F, int64_t K) { return here(dtype, F, K, 2); }
+size_t glu_prod_bytes(int dtype, int64_t M, int64_t F, int64_t K) {
     if (M == 0 || F == 0 || K == 0) return 0;
     size_t most = 0;
-    const int dx = dx_parts(M, F, K);
+    const int dx = dx_parts(dtype, M, F, K);
     if (dx > 1) most = (size_t)dx * M * K * 4;
-    for (int c = 1; c <= 2; ++c) {
-        const int dw = dw_parts(M, F, K, c);
-        if (dw > 1 && (size_t)dw * c * F * K * 4 > most) most = (size_t)dw * c * F * K * 4;
-    }
+    const int dw = dw_parts(dtype, M, F, K);
+    if (dw > 1 && (size_t)dw * 2 * F * K * 4 > most) most = (size_t)dw * 2 * F * K * 4;
     return most;
 }
 
@@ -349,7 +369,7 @@ hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s) {
         const int64_t wgs64 = cdiv(a.M, 64) * cdiv(a.F, 32), wgs32 = cdiv(a.M, 32) * cdiv(a.F, 32);
         if (a.M <= 32 || wgs32 <= 256) return launch_glu_rows<T, 32>(a, dma, s);
         if (a.M <= 64 || wgs64 <= 256) return launch_glu_rows<T, 64>(a, dma, s);
-        return with_tile(dtype, a.K, dma, false, a.M, 2 * (int64_t)a.F, 1, cdiv(a.K, Elem<T>::SLICE), [&](auto tile) {
+        return with_tile<false>(dtype, a.K, dma, a.M, 2 * (int64_t)a.F, 1, cdiv(a.K, Elem<T>::SLICE), [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.F, Tl::BN / 2);
             hipLaunchKernelGGL((k_glu_fwd<T, Tl>), dim3((unsigned)((int64_t)tm * tn)), dim3(Tl::NT), 0, s, a, tm,
@@ -364,10 +384,13 @@ int check_glu_prod(const GluProdArgs& a) {
     return x <= max_workgroups(512) && w <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
-template <class Fn>
-static hipError_t with_half(int dtype, Fn&& f) {
-    if (dtype == SGEMM_F32_DTYPE_BF16) return f(TypeTag<bf16>{});
-    return f(TypeTag<f16>{});
+// The tile of a backward product in n parts.
+template <class T, class Fn>
+static hipError_t pick(int dtype, int n, int K, bool dma, int64_t rows, int64_t cols, int64_t copies, int64_t slices,
+                       Fn&& f) {
+    if constexpr (sizeof(T) == 2)
+        if (n == 1) return with_tile<false>(dtype, K, dma, rows, cols, copies, slices, f);
+    return with_tile<true>(dtype, K, dma, rows, cols, copies, slices, f);
 }
 
 template <class T>
@@ -380,16 +403,17 @@ hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s) {
     // One tile's lines: 256 rows of dG, or a slice's 64 of W.
     const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 256) && dma_ok(dtype, a.W[0], a.ldw[0], a.K, 64) &&
                      dma_ok(dtype, a.W[1], a.ldw[1], a.K, 64) && a.ldw[0] == a.ldw[1];
-    const int n = dx_parts(a.M, a.F, a.K);
-    return with_half(dtype, [&](auto tag) {
+    const int n = dx_parts(dtype, a.M, a.F, a.K);
+    return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        const hipError_t e = with_tile(dtype, a.K, dma, n > 1, a.M, a.K, 1, 2 * cdiv(a.F, 64), [&](auto tile) {
+        auto go = [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.M, Tl::BM), tn = (int)cdiv(a.K, Tl::BN);
             hipLaunchKernelGGL((k_glu_dx<T, Tl>), dim3((unsigned)((int64_t)tm * tn), 1, (unsigned)n), dim3(Tl::NT),
                                0, s, a, tm, tn, xcd_remap_enabled());
             return hipGetLastError();
-        });
+        };
+        const hipError_t e = pick<T>(dtype, n, a.K, dma, a.M, a.K, 1, 2 * cdiv(a.F, slice_of(dtype)), go);
         return e != hipSuccess || n == 1 ? e : launch_sum<T>(a, a.M, 1, n, s);
     });
 }
@@ -397,16 +421,17 @@ hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s) {
 hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s) {
     const unsigned both = a.C[0] != nullptr && a.C[1] != nullptr ? 2 : 1;
     const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 64) && dma_ok(dtype, a.X, a.ldx, a.K, 64);
-    const int n = dw_parts(a.M, a.F, a.K, (int)both);
-    return with_half(dtype, [&](auto tag) {
+    const int n = dw_parts(dtype, a.M, a.F, a.K);
+    return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        const hipError_t e = with_tile(dtype, a.K, dma, n > 1, a.F, a.K, both, cdiv(a.M, 64), [&](auto tile) {
+        auto go = [&](auto tile) {
             using Tl = typename decltype(tile)::type;
             const int tm = (int)cdiv(a.F, Tl::BM), tn = (int)cdiv(a.K, Tl::BN);
             hipLaunchKernelGGL((k_glu_dw<T, Tl>), dim3((unsigned)((int64_t)tm * tn), both, (unsigned)n),
                                dim3(Tl::NT), 0, s, a, tm, tn, xcd_remap_enabled());
             return hipGetLastError();
-        });
+        };
+        const hipError_t e = pick<T>(dtype, n, a.K, dma, a.F, a.K, 2, cdiv(a.M, slice_of(dtype)), go);
         return e != hipSuccess || n == 1 ? e : launch_sum<T>(a, a.F, both, n, s);
     });
 }

@@ -87,8 +87,10 @@ def test_glu_whole_numbers(dev, shape, dtype, layout):
 
 
 # Enough tiles for the largest block tile in each product (H: M x 2F, dX:
-# M x K, dW: F x K), with ragged edges in whole 16-byte chunks.
-LARGE = [(3000, 4136, 144), (2904, 72, 4200), (72, 2600, 2728), (520, 264, 200)]
+# M x K, dW: F x K) with ragged edges in whole 16-byte chunks, products
+# split over their slices (few tiles, long sums), and odd ones of both kinds.
+LARGE = [(3000, 4136, 144), (2904, 72, 4200), (72, 2600, 2728), (520, 264, 200), (100, 3001, 130),
+         (2500, 65, 67), (1201, 1203, 1205), (2050, 2048, 8)]
 
 
 @pytest.mark.parametrize("dtype", ref.DTYPES)
@@ -217,13 +219,14 @@ def test_glu_backward_against_differences(dev, act):
         assert abs((g.double() * d).sum() - slope) <= (b * d.abs()).sum() + 1e-6, i
 
 
+@pytest.mark.parametrize("shape", [(40, 70, 90), (1500, 200, 300), (300, 1500, 1200)], ids=str)
 @pytest.mark.parametrize("dtype", ref.DTYPES)
-def test_glu_backward_parts(dev, dtype):
+def test_glu_backward_parts(dev, dtype, shape):
     # Any of the three alone gives the same bits as all of them.
     t = ref.DTYPES[dtype]
-    M, F, K = 40, 70, 90
-    _say("glu_backward parts", dtype)
-    gen = _gen(6)
+    M, F, K = shape
+    _say("glu_backward parts", dtype, shape)
+    gen = _gen(6, shape)
     X, dH = _normal((M, K), gen, dev, t), _normal((M, F), gen, dev, t)
     Wg, Wu = (_normal((F, K), gen, dev, t, 0.1) for _ in range(2))
     P = torch.empty(M, 2 * F, device=dev)
