@@ -246,21 +246,8 @@ struct WaveMap {
                             v += space[mn + g * WAVES][((i * BJ + j) * 16 + kk * REGS + r) * 64 + lane];
                         acc[i][j][r] = v;
                     }
+            __syncthreads();   // the space is free again
         }
-    }
-    // f(block row, block column, register, tile row, tile column) of this wave's results.
-    template <class Fn>
-    __device__ __forceinline__ void each(Fn&& f) const {
-#pragma unroll
-        for (int bi = 0; bi < BI; ++bi)
-#pragma unroll
-            for (int bj = 0; bj < BJ; ++bj)
-#pragma unroll
-                for (int r = 0; r < REGS; ++r) {
-                    const int rr = kk * REGS + r;
-                    f(bi, bj, r, wm + 32 * bi + 8 * (rr >> 2) + 4 * (lane >> 5) + (rr & 3),
-                      wn + 32 * bj + (lane & 31));
-                }
     }
 };
 
@@ -270,6 +257,7 @@ struct TileCore {
     static constexpr int NT = Map::WAVES * KS * 64;
     static constexpr int BI = WM / 32, BJ = WN / 32;
     static constexpr int STAGE = (BM + BN) * 128;
+    static constexpr int PER_WAVE = 2 * STAGE / (Map::WAVES * KS);   // LDS of a wave's own, the product done
 
     template <class Src>
     __device__ __forceinline__ static void run(char* lds, int m0, int n0, int s_begin, int s_end, Src&& src,
@@ -313,7 +301,7 @@ struct TileCore {
 #pragma unroll
                 for (int i = 0; i < BI; ++i)
 #pragma unroll
-                    for (int j = 0; j < BJ; ++j) mma_chunk(T{}, a[i], b[j], acc[i][j]);
+                    for (int j = 0; j < BJ; ++j) mma_chunk(T{}, b[j], a[i], acc[i][j]);
             }
         };
         Set r0, r1;
@@ -434,6 +422,13 @@ struct DmaCore {
     static constexpr int NT = Map::WAVES * KS * 64;
     static constexpr int BI = WM / 32, BJ = WN / 32;
     static constexpr int LDS_A = BM * 128, LDS_B = BN * 128;
+    // LDS of a wave's own once the product is done.
+    static constexpr int WAVES = Map::WAVES * KS, PER_WAVE = 2 * (LDS_A + LDS_B) / WAVES;
+    static_assert(LDS_A == LDS_B && WAVES % 4 == 0, "four equal objects, whole waves in each");
+    __device__ __forceinline__ static char* own(char* a0, char* b0, char* a1, char* b1) {
+        const int w = threadIdx.x >> 6, o = w / (WAVES / 4);
+        return (o == 0 ? a0 : o == 1 ? b0 : o == 2 ? a1 : b1) + w % (WAVES / 4) * PER_WAVE;
+    }
     using FA = DmaFill<T, BM, NT, ARC>;
     using FB = DmaFill<T, BN, NT, BRC>;
 
@@ -496,7 +491,7 @@ struct DmaCore {
 #pragma unroll
             for (int i = 0; i < BI; ++i)
 #pragma unroll
-                for (int j = 0; j < BJ; ++j) mma_chunk(T{}, f.a[i], f.b[j], acc[i][j]);
+                for (int j = 0; j < BJ; ++j) mma_chunk(T{}, f.b[j], f.a[i], acc[i][j]);
         };
         Frag f0, f1;
         issue(s_begin, a0, b0);
@@ -545,5 +540,51 @@ __device__ __forceinline__ void wave_wait() {
     __builtin_amdgcn_s_waitcnt((VMCNT & 15) | ((VMCNT >> 4) << 14) | (7 << 4) | (15 << 8));
     asm volatile("" ::: "memory");
 }
+
+// One block row of a wave's results on its way out: 32 rows of COLS columns of
+// type O, through LDS of the wave's own (no barrier), so that a store
+// instruction writes whole runs of rows, 16 bytes a lane. The matrix instructions take
+// the column operand first, so a lane's registers run along a row: lane l holds
+// row l % 32, register group r of a block its columns 8 r + 4 (l / 32) + 0..3.
+// (Stored from the registers, those 16 or 8 bytes of each of 32 rows a time, the
+// FP32 pre-activations of 4096 x 8192 outputs cost 140 us more.)
+template <class O, int COLS>
+struct RowsOut {
+    static constexpr int PITCH = COLS * (int)sizeof(O) + 16;   // bytes; rows 16 bytes apart in the banks
+    static constexpr int BYTES = 32 * PITCH;
+    static constexpr int EPC = 16 / (int)sizeof(O), LPR = COLS / EPC;   // lanes per row
+    typedef O O4 __attribute__((ext_vector_type(4)));
+    char* lds;
+    int lane;
+
+    __device__ __forceinline__ void put(int col, float a, float b, float c, float d) const {
+        *(O4*)(lds + (lane & 31) * PITCH + (col + 4 * (lane >> 5)) * (int)sizeof(O)) = O4{(O)a, (O)b, (O)c, (O)d};
+    }
+    // To rows row0 .. of a matrix whose first column here is `out`'s; `rows` and
+    // `cols` of them exist.
+    __device__ __forceinline__ void flush(O* out, int64_t ld, int row0, int rows, int cols) const {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+        typedef O E __attribute__((ext_vector_type(EPC)));
+        typedef E Eu __attribute__((aligned(sizeof(O))));
+#pragma unroll
+        for (int i = 0; i < 32 * LPR / 64; ++i) {
+            const int at = i * 64 + lane, row = at / LPR, col = at % LPR * EPC;
+            const E v = *(const E*)(lds + row * PITCH + col * (int)sizeof(O));
+            O* p = out + (int64_t)(row0 + row) * ld + col;
+            if (row0 + row < rows && col < cols) {
+                if (col + EPC <= cols) {
+                    *(Eu*)p = v;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < EPC - 1; ++k)
+                        if (col + k < cols) p[k] = v[k];
+                }
+            }
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+    }
+};
 
 }  // namespace sgemm

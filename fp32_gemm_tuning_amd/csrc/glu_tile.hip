@@ -6,21 +6,24 @@
 
 namespace sgemm {
 
-constexpr int GLU_GROUP_M = 8;
+constexpr int GLU_GROUP_M = 4;
 
 // A core's product in LDS of its own: two stages for each operand, as objects
 // apart so that the compiler can tell the stage being filled from the one
 // being read.
+// Returns LDS of the wave's own for the results.
 template <class Core, bool DMA, class Src>
-__device__ __forceinline__ void product(int m0, int n0, int s_begin, int s_end, Src&& src,
+__device__ __forceinline__ char* product(int m0, int n0, int s_begin, int s_end, Src&& src,
                                         f32x16 (&acc)[Core::BI][Core::BJ]) {
     if constexpr (DMA) {
         __shared__ __attribute__((aligned(16))) char a0[Core::LDS_A], b0[Core::LDS_B], a1[Core::LDS_A],
             b1[Core::LDS_B];
         Core::run(a0, b0, a1, b1, m0, n0, s_begin, s_end, src, acc);
+        return Core::own(a0, b0, a1, b1);
     } else {
         __shared__ __attribute__((aligned(16))) char lds[2 * Core::STAGE];
         Core::run(lds, m0, n0, s_begin, s_end, src, acc);
+        return lds + (threadIdx.x >> 6) * Core::PER_WAVE;
     }
 }
 
@@ -53,18 +56,38 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_fwd(GluArgs a, int tiles_m, int 
         lb[1] = Lines<T>{(const T*)a.Wu, a.ldwu, a.F, a.K};
         return s * Elem<T>::SLICE;
     };
-    product<Core, Tl::DMA>(m0, f0, 0, (a.K + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
-    typename Tl::Map().each([&](int bi, int bj, int r, int i, int j) {
-        if (bj & 1) return;
-        const int row = m0 + i, f = f0 + (j >> 6) * 32 + (j & 31);
-        if (row >= a.M || f >= a.F) return;
-        const float g = acc[bi][bj][r], u = acc[bi][bj + 1][r];
-        ((T*)a.H)[(int64_t)row * a.ldh + f] = (T)(act_value<sizeof(T) == 4>(a.act, g) * u);
-        if (a.P != nullptr) {
-            a.P[(int64_t)row * a.ldp + f] = g;
-            a.P[(int64_t)row * a.ldp + a.F + f] = u;
+    char* const own = product<Core, Tl::DMA>(m0, f0, 0, (a.K + Elem<T>::SLICE - 1) / Elem<T>::SLICE, src, acc);
+    // Block by block: 32 rows of the 32 (KS = 2: 16) features of a pair.
+    const typename Tl::Map map;
+    constexpr int REGS = Tl::Map::REGS, COLS = 2 * REGS;
+    const RowsOut<T, COLS> h = {own, map.lane};
+    const RowsOut<float, COLS> pg = {own, map.lane}, pu = {own + RowsOut<float, COLS>::BYTES, map.lane};
+    static_assert(Core::PER_WAVE >= 2 * RowsOut<float, COLS>::BYTES, "staging");
+#pragma unroll
+    for (int bi = 0; bi < Core::BI; ++bi)
+#pragma unroll
+        for (int bj = 0; bj < Core::BJ; bj += 2) {
+            const int row = m0 + map.wm + 32 * bi;
+            const int f = f0 + ((map.wn + 32 * bj) >> 1) + COLS * map.kk;
+            const f32x16 &g = acc[bi][bj], &u = acc[bi][bj + 1];
+            if (a.P != nullptr) {
+#pragma unroll
+                for (int r = 0; r < REGS; r += 4) {
+                    pg.put(2 * r, g[r], g[r + 1], g[r + 2], g[r + 3]);
+                    pu.put(2 * r, u[r], u[r + 1], u[r + 2], u[r + 3]);
+                }
+                pg.flush(a.P + f, a.ldp, row, a.M, a.F - f);
+                pu.flush(a.P + a.F + f, a.ldp, row, a.M, a.F - f);
+            }
+#pragma unroll
+            for (int r = 0; r < REGS; r += 4) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = act_value<sizeof(T) == 4>(a.act, g[r + e]) * u[r + e];
+                h.put(2 * r, v[0], v[1], v[2], v[3]);
+            }
+            h.flush((T*)a.H + f, a.ldh, row, a.M, a.F - f);
         }
-    });
 }
 
 // The forward pass of few rows: the weights' bytes are the work. A workgroup takes
@@ -176,12 +199,38 @@ __global__ __launch_bounds__(KW * 64) void k_glu_rows(GluArgs a) {
 
 // Where a backward product's sums go: the result, or, split over its slices
 // (blockIdx.z of gridDim.z parts), FP32 partial sums that k_glu_sum adds in order.
-template <class T>
-__device__ __forceinline__ void put(const GluProdArgs& a, int u, int64_t rows, int row, int col, float v) {
+// A wave's blocks of a block row go out together where their columns are
+// next to each other (KS = 1).
+template <class O, class Tl, class Core>
+__device__ __forceinline__ void put_rows(char* own, O* out, int64_t ld, int m0, int n0, int rows, int cols,
+                                         const f32x16 (&acc)[Core::BI][Core::BJ]) {
+    const typename Tl::Map map;
+    constexpr int REGS = Tl::Map::REGS, KS = 16 / REGS, TOGETHER = KS == 1 ? Core::BJ : 1, COLS = 2 * REGS * TOGETHER;
+    const RowsOut<O, COLS> o = {own, map.lane};
+    static_assert(RowsOut<O, COLS>::BYTES <= Core::PER_WAVE, "staging");
+#pragma unroll
+    for (int bi = 0; bi < Core::BI; ++bi)
+#pragma unroll
+        for (int bj = 0; bj < Core::BJ; bj += TOGETHER) {
+            const int col = n0 + map.wn + 32 * bj + 2 * REGS * map.kk;
+#pragma unroll
+            for (int j = 0; j < TOGETHER; ++j)
+#pragma unroll
+                for (int r = 0; r < REGS; r += 4) {
+                    const f32x16& v = acc[bi][bj + j];
+                    o.put(32 * j + 2 * r, v[r], v[r + 1], v[r + 2], v[r + 3]);
+                }
+            o.flush(out + col, ld, m0 + map.wm + 32 * bi, rows, cols - col);
+        }
+}
+template <class T, class Tl, class Core>
+__device__ __forceinline__ void put(const GluProdArgs& a, int u, int rows, int m0, int n0, char* own,
+                                    const f32x16 (&acc)[Core::BI][Core::BJ]) {
     if (gridDim.z > 1)
-        a.part[((int64_t)(blockIdx.z * gridDim.y + blockIdx.y) * rows + row) * a.K + col] = v;
+        put_rows<float, Tl, Core>(own, a.part + (int64_t)(blockIdx.z * gridDim.y + blockIdx.y) * rows * a.K, a.K, m0, n0,
+                                  rows, a.K, acc);
     else
-        ((T*)(u ? a.C[1] : a.C[0]))[(int64_t)row * (u ? a.ldc[1] : a.ldc[0]) + col] = (T)v;
+        put_rows<T, Tl, Core>(own, (T*)(u ? a.C[1] : a.C[0]), u ? a.ldc[1] : a.ldc[0], m0, n0, rows, a.K, acc);
 }
 // This part's slices of n.
 __device__ __forceinline__ void part_of(int n, int& begin, int& end) {
@@ -209,11 +258,8 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, i
         if (!Tl::DMA) lb[0].ld = u ? a.ldw[1] : a.ldw[0];
         return (s - u * half) * Elem<T>::SLICE;
     };
-    product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
-    typename Tl::Map().each([&](int bi, int bj, int r, int i, int j) {
-        const int row = m0 + i, col = n0 + j;
-        if (row < a.M && col < a.K) put<T>(a, 0, a.M, row, col, acc[bi][bj][r]);
-    });
+    char* const own = product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
+    put<T, Tl, Core>(a, 0, a.M, m0, n0, own, acc);
 }
 
 // dWg = dG^T X (blockIdx.y 0) and dWu = dU^T X (1): sums over the M tokens.
@@ -231,11 +277,8 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dw(GluProdArgs a, int tiles_m, i
         lb[0] = Lines<T>{(const T*)a.X, a.ldx, a.M, a.K};
         return s * Elem<T>::SLICE;
     };
-    product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
-    typename Tl::Map().each([&](int bi, int bj, int r, int i, int j) {
-        const int f = m0 + i, col = n0 + j;
-        if (f < a.F && col < a.K) put<T>(a, u, a.F, f, col, acc[bi][bj][r]);
-    });
+    char* const own = product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
+    put<T, Tl, Core>(a, u, a.F, m0, n0, own, acc);
 }
 
 // The sums of a split product's parts, in their order.

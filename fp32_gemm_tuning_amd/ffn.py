@@ -34,6 +34,11 @@ from typing import NamedTuple, Optional, Tuple
 
 from . import SgemmError, _lib, _ptr, _stream
 
+try:
+    import torch
+except ImportError:   # the C-ABI mirrors need no torch
+    torch = None
+
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = 0, 1, 2, 3
 ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU}
@@ -111,17 +116,15 @@ class W4(NamedTuple):
     group: int
 
 
-_dtypes = {}
-_raw_stream = None   # device index -> address of its current stream
+if torch is not None:
+    _dtypes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    # device index -> address of its current stream
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _dtype(t, name: str) -> int:
-    global _raw_stream
-    if not _dtypes:
-        import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda index: torch.cuda.current_stream(index).cuda_stream)
-        _dtypes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
     d = _dtypes.get(t.dtype)
     if d is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
@@ -170,9 +173,8 @@ _entries = {name: getattr(_lib, name) for name in _SIGNATURES}
 
 def _call(like, stream, entry: str, *args) -> None:
     """Calls the C entry point with `like`'s device current."""
-    import torch
     index = like.get_device()
-    if torch.cuda.current_device() == index:
+    if _device() == index:
         rc = _entries[entry](*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(index):
@@ -195,8 +197,7 @@ def glu(X, Wg, Wu, act: str = "silu", out=None, preact=None, stream=None):
     t = X.dtype
     ldp = 2 * F
     if preact is not None:
-        import torch
-        ldp = _ld(preact, X, torch.float32, M, 2 * F, "preact")
+            ldp = _ld(preact, X, torch.float32, M, 2 * F, "preact")
     _call(X, stream, "sgemm_f32_glu", d, _act(act), M, F, K, X.data_ptr(), _ld(X, X, t, M, K, "X"),
           Wg.data_ptr(), _ld(Wg, X, t, F, K, "Wg"), Wu.data_ptr(), _ld(Wu, X, t, F, K, "Wu"), H.data_ptr(),
           _ld(H, X, t, M, F, "out"), None if preact is None else preact.data_ptr(), max(ldp, 1))
@@ -209,7 +210,6 @@ def glu_backward(dH, X, Wg, Wu, preact, act: str = "silu", dX=None, dWg=None, dW
     filled. Each of the three is written where a tensor is given, allocated
     where it is None, and left out (None in the result) where it is False.
     `workspace`: a CUDA tensor of at least glu_backward_workspace() bytes."""
-    import torch
     d = _gpu(X, "X")
     M, K = X.shape
     F = Wg.shape[0]
@@ -245,8 +245,7 @@ def glu_backward_workspace(X, F: int) -> int:
     d = _gpu(X, "X")
     cus = _cus.get(X.get_device())
     if cus is None:
-        import torch
-        cus = _cus[X.get_device()] = torch.cuda.get_device_properties(X.device).multi_processor_count
+            cus = _cus[X.get_device()] = torch.cuda.get_device_properties(X.device).multi_processor_count
     rc, need = sgemm_f32_glu_bwd_ws_size(d, X.shape[0], F, X.shape[1], cus)
     if rc != 0:
         raise SgemmError(rc, "sgemm_f32_glu_bwd_ws_size")
@@ -261,7 +260,6 @@ def _groups(K: int, group: int) -> int:
 
 def _w4(w: W4, like, name: str):
     """(F, the C arguments) of a 4-bit weight matrix."""
-    import torch
     F, G = w.q.shape[0], _groups(w.K, w.group)
     if w.q.dim() != 2 or w.q.shape[1] != (w.K + 1) // 2:
         raise ValueError(f"{name}.q must have shape (F, {(w.K + 1) // 2}), got {tuple(w.q.shape)}")
@@ -274,7 +272,6 @@ def _w4(w: W4, like, name: str):
 
 def w4_quantize(W, group: int = 128, zeros: bool = False, stream=None) -> W4:
     """W (F, K) in 4 bits, with zero points where `zeros`."""
-    import torch
     d = _gpu(W, "W")
     F, K = W.shape
     G = _groups(K, group)
