@@ -102,6 +102,10 @@ struct GluGradArgs {
     const void* dH;
     void* dG;
     void* dU;
+    // What the rounding of dG and dU left, rounded itself (glu_two_parts), or
+    // null.
+    void* dGl;
+    void* dUl;
     int64_t ldp, lddh, ldd;
     int32_t M, F;
     int32_t act;
@@ -113,6 +117,7 @@ struct GluGradArgs {
 // (glu_prod_bytes).
 struct GluProdArgs {
     const void* D[2];
+    const void* L[2];   // their second parts, summed after them, or null
     const void* W[2];
     const void* X;
     void* C[2];
@@ -148,6 +153,15 @@ struct PackArgs {
 int check_glu(const GluArgs& a);
 hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s);
 int check_glu_prod(const GluProdArgs& a);
+// Whether a 16-bit backward pass keeps dG and dU in two parts: where few
+// values carry the sums, the roundings of single ones show in the gradients
+// instead of averaging out (one part: the error's norm is 1.41 times that of
+// rounding the gradients alone, give or take 2% at 16384 values, and 1.5 times and
+// more for a few hundred; two parts: 1.00 times). The doubled sums
+// are small there.
+static inline bool glu_two_parts(int dtype, int64_t M, int64_t F) {
+    return dtype != SGEMM_F32_DTYPE_F32 && M * F <= 16384;
+}
 // Whether the backward products of these sizes run on launch_glu_dx and
 // launch_glu_dw (16-bit ones do) or, FP32, on sgemm_f32_ws.
 bool glu_dx_here(int dtype, int64_t M, int64_t K);

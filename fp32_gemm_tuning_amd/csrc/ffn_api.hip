@@ -41,17 +41,17 @@ int32_t group_of(int64_t group, int64_t K) {
 
 // The backward pass's workspace: dG and dU, each M rows of ldd elements (F
 // rounded up to whole 64-element slices, so that their rows are whole 16-byte
-// chunks), then the partial sums of products that are split, or, for large
+// chunks), where they are kept in two parts their second ones, then the partial sums of products that are split, or, for large
 // FP32 products, what the stream-K kernels may use.
 struct BwdSpace {
     int64_t ldd;
-    size_t du_at, sk_at, sk_bytes, total;
+    size_t one, sk_at, sk_bytes, total;   // dG at 0, the others `one` apart
 };
 int bwd_space(int dtype, int64_t M, int64_t F, int64_t K, int num_cus, BwdSpace* o) {
     o->ldd = cdiv(F > 0 ? F : 1, 64) * 64;
     const size_t one = up256((size_t)M * (size_t)o->ldd * (size_t)dtype_bytes(dtype));
-    o->du_at = one;
-    o->sk_at = 2 * one;
+    o->one = one;
+    o->sk_at = (glu_two_parts(dtype, M, F) ? 4 : 2) * one;
     size_t most = glu_prod_bytes(dtype, M, F, K);
     if (dtype == SGEMM_F32_DTYPE_F32) {
         size_t dx = 0, dw = 0;
@@ -204,9 +204,11 @@ SGEMM_F32_API int sgemm_f32_glu_bwd(int dtype, int act, int64_t M, int64_t F, in
     char* const ws = (char*)workspace;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
 
-    GluProdArgs p = {{ws, ws + sp.du_at}, {Wg, Wu}, X, {nullptr, nullptr}, (float*)(ws + sp.sk_at), sp.ldd, {ldwg, ldwu}, ldx,
+    const bool two = glu_two_parts(dtype, M, F);
+    char* const second[2] = {two ? ws + 2 * sp.one : nullptr, two ? ws + 3 * sp.one : nullptr};
+    GluProdArgs p = {{ws, ws + sp.one}, {second[0], second[1]}, {Wg, Wu}, X, {nullptr, nullptr}, (float*)(ws + sp.sk_at), sp.ldd, {ldwg, ldwu}, ldx,
                      {0, 0}, (int32_t)M, (int32_t)F, (int32_t)K};
-    const GluGradArgs g = {P, dH, ws, ws + sp.du_at, ldp, lddh, sp.ldd, (int32_t)M, (int32_t)F, act};
+    const GluGradArgs g = {P, dH, ws, ws + sp.one, second[0], second[1], ldp, lddh, sp.ldd, (int32_t)M, (int32_t)F, act};
     rc = check_glu_grad(g);
     if (rc == 0) rc = check_glu_prod(p);
     if (rc) return rc;

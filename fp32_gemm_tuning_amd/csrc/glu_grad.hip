@@ -17,7 +17,7 @@ __global__ __launch_bounds__(256) void k_glu_grad(GluGradArgs a) {
     const int64_t row = at / a.ldd;
     const int col = (int)(at - row * a.ldd);
     if (row >= a.M) return;
-    T4 dg = {}, du = {};
+    T4 dg = {}, du = {}, dgl = {}, dul = {};
     const float* p = a.P + row * a.ldp + col;
     const T* h = (const T*)a.dH + row * a.lddh + col;
     f32x4 g = {}, u = {};
@@ -39,11 +39,20 @@ __global__ __launch_bounds__(256) void k_glu_grad(GluGradArgs a) {
     for (int e = 0; e < 4; ++e) {
         if (col + e >= a.F) break;
         const float d = (float)dh[e];
-        du[e] = (T)(d * act_value<sizeof(T) == 4>(a.act, g[e]));
-        dg[e] = (T)(d * u[e] * act_slope<sizeof(T) == 4>(a.act, g[e]));
+        const float vu = d * act_value<sizeof(T) == 4>(a.act, g[e]);
+        const float vg = d * u[e] * act_slope<sizeof(T) == 4>(a.act, g[e]);
+        du[e] = (T)vu;
+        dg[e] = (T)vg;
+        const float ru = vu - (float)du[e], rg = vg - (float)dg[e];
+        dul[e] = (T)(fabsf(ru) <= 3.0e38f ? ru : 0.0f);   // (nothing is left of an infinity or NaN)
+        dgl[e] = (T)(fabsf(rg) <= 3.0e38f ? rg : 0.0f);
     }
     *(T4*)((T*)a.dG + at) = dg;
     *(T4*)((T*)a.dU + at) = du;
+    if (a.dGl != nullptr) {
+        *(T4*)((T*)a.dGl + at) = dgl;
+        *(T4*)((T*)a.dUl + at) = dul;
+    }
 }
 
 static int64_t workgroups(const GluGradArgs& a) { return ((int64_t)a.M * a.ldd / 4 + 255) / 256; }

@@ -240,7 +240,7 @@ __device__ __forceinline__ void part_of(int n, int& begin, int& end) {
 }
 
 // dX = dG Wg + dU Wu as one sum over 2F: first the slices of dG and Wg, then
-// those of dU and Wu.
+// those of dU and Wu; then, where dG and dU have second parts, the same with those.
 template <class T, class Tl>
 __global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, int tiles_n, int xcd) {
     using Core = typename Tl::template Core<T, false, true, false>;
@@ -248,12 +248,15 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, i
     tile_of(blockIdx.x, tiles_m, tiles_n, GLU_GROUP_M, xcd != 0, tm, tn);
     const int m0 = __builtin_amdgcn_readfirstlane(tm * Tl::BM), n0 = __builtin_amdgcn_readfirstlane(tn * Tl::BN);
     const int half = (a.F + Elem<T>::SLICE - 1) / Elem<T>::SLICE;
-    part_of(2 * half, s0, s1);
+    part_of(a.L[0] != nullptr ? 4 * half : 2 * half, s0, s1);
     f32x16 acc[Core::BI][Core::BJ];
     auto src = [&](int s, Lines<T>& la, Lines<T>* lb) {
+        // (slices past the last one are asked for too: their k lies past the sums)
+        const bool second = a.L[0] != nullptr && s >= 2 * half;
+        if (second) s -= 2 * half;
         const int u = s >= half;
         // (dG and dU are zero from F to whole slices)
-        la = Lines<T>{(const T*)(u ? a.D[1] : a.D[0]), a.ldd, a.M, half * Elem<T>::SLICE};
+        la = Lines<T>{(const T*)(second ? (u ? a.L[1] : a.L[0]) : (u ? a.D[1] : a.D[0])), a.ldd, a.M, half * Elem<T>::SLICE};
         lb[0] = Lines<T>{(const T*)(u ? a.W[1] : a.W[0]), a.ldw[0], a.F, a.K};
         if (!Tl::DMA) lb[0].ld = u ? a.ldw[1] : a.ldw[0];
         return (s - u * half) * Elem<T>::SLICE;
@@ -262,7 +265,8 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, i
     put<T, Tl, Core>(a, 0, a.M, m0, n0, own, acc);
 }
 
-// dWg = dG^T X (blockIdx.y 0) and dWu = dU^T X (1): sums over the M tokens.
+// dWg = dG^T X (blockIdx.y 0) and dWu = dU^T X (1): sums over the M tokens, of
+// the second parts after the first where there are any.
 template <class T, class Tl>
 __global__ __launch_bounds__(Tl::NT) void k_glu_dw(GluProdArgs a, int tiles_m, int tiles_n, int xcd) {
     using Core = typename Tl::template Core<T, true, true, false>;
@@ -270,10 +274,14 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dw(GluProdArgs a, int tiles_m, i
     int tm, tn, s0, s1;
     tile_of(blockIdx.x, tiles_m, tiles_n, GLU_GROUP_M, xcd != 0, tm, tn);
     const int m0 = __builtin_amdgcn_readfirstlane(tm * Tl::BM), n0 = __builtin_amdgcn_readfirstlane(tn * Tl::BN);
-    part_of((a.M + Elem<T>::SLICE - 1) / Elem<T>::SLICE, s0, s1);
+    const int once = (a.M + Elem<T>::SLICE - 1) / Elem<T>::SLICE;
+    part_of(a.L[0] != nullptr ? 2 * once : once, s0, s1);
     f32x16 acc[Core::BI][Core::BJ];
     auto src = [&](int s, Lines<T>& la, Lines<T>* lb) {
-        la = Lines<T>{(const T*)(u ? a.D[1] : a.D[0]), a.ldd, a.M, (a.F + 63) / 64 * 64};
+        const bool second = a.L[0] != nullptr && s >= once;
+        if (second) s -= once;
+        la = Lines<T>{(const T*)(second ? (u ? a.L[1] : a.L[0]) : (u ? a.D[1] : a.D[0])), a.ldd, a.M,
+                      (a.F + 63) / 64 * 64};
         lb[0] = Lines<T>{(const T*)a.X, a.ldx, a.M, a.K};
         return s * Elem<T>::SLICE;
     };
@@ -359,12 +367,18 @@ static int parts(int64_t rows, int64_t cols, int64_t copies, int64_t slices, int
     return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
 static int64_t slice_of(int dtype) { return 128 / dtype_bytes(dtype); }
+static int64_t dx_slices(int dtype, int64_t M, int64_t F) {
+    return (glu_two_parts(dtype, M, F) ? 4 : 2) * cdiv(F, slice_of(dtype));
+}
+static int64_t dw_slices(int dtype, int64_t M, int64_t F) {
+    return (glu_two_parts(dtype, M, F) ? 2 : 1) * cdiv(M, slice_of(dtype));
+}
 static int dx_parts(int dtype, int64_t M, int64_t F, int64_t K) {
-    return parts(M, K, 1, 2 * cdiv(F, slice_of(dtype)), (int)K);
+    return parts(M, K, 1, dx_slices(dtype, M, F), (int)K);
 }
 // (as for both gradients, so that one alone has the same bits)
 static int dw_parts(int dtype, int64_t M, int64_t F, int64_t K) {
-    return parts(F, K, 2, cdiv(M, slice_of(dtype)), (int)K);
+    return parts(F, K, 2, dw_slices(dtype, M, F), (int)K);
 }
 // FP32 products up to 640 tiles run here, larger ones on the library's own dispatch
 // (tiles of 64 x 64: dX of 77 x 1000 x 511 16.4 us against 18.3, 1000 x 1531 x 777 83
@@ -456,7 +470,7 @@ hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s) {
                                0, s, a, tm, tn, xcd_remap_enabled());
             return hipGetLastError();
         };
-        const hipError_t e = pick<T>(dtype, n, a.K, dma, a.M, a.K, 1, 2 * cdiv(a.F, slice_of(dtype)), go);
+        const hipError_t e = pick<T>(dtype, n, a.K, dma, a.M, a.K, 1, dx_slices(dtype, a.M, a.F), go);
         return e != hipSuccess || n == 1 ? e : launch_sum<T>(a, a.M, 1, n, s);
     });
 }
@@ -474,7 +488,7 @@ hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s) {
                                dim3(Tl::NT), 0, s, a, tm, tn, xcd_remap_enabled());
             return hipGetLastError();
         };
-        const hipError_t e = pick<T>(dtype, n, a.K, dma, a.F, a.K, 2, cdiv(a.M, slice_of(dtype)), go);
+        const hipError_t e = pick<T>(dtype, n, a.K, dma, a.F, a.K, 2, dw_slices(dtype, a.M, a.F), go);
         return e != hipSuccess || n == 1 ? e : launch_sum<T>(a, a.F, both, n, s);
     });
 }

@@ -69,8 +69,11 @@ def glu_grads(dH, X, Wg, Wu, kind):
 def glu_grads_bounds(dH, X, Wg, Wu, kind, dtype):
     """Elementwise bounds for dX, dWg and dWu (smooth activations: second
     derivatives are at most 1 in magnitude). dG and dU are rounded once to the
-    type, then summed in FP32, and the sums rounded once."""
+    type, then summed in FP32, and the sums rounded once. Up to 16384 values dG
+    and dU are kept in two parts, the second a rounding of what the first left:
+    their error is half a step of half a step."""
     r, t = HALF_STEP[dtype], TINY[dtype]
+    rd = r * r if dtype != "f32" and dH.numel() <= 16384 else r
     g, u = X @ Wg.T, X @ Wu.T
     e = sum_error(X.shape[1])
     eg, eu = e * (X.abs() @ Wg.abs().T), e * (X.abs() @ Wu.abs().T)
@@ -82,8 +85,8 @@ def glu_grads_bounds(dH, X, Wg, Wu, kind, dtype):
     edg = h * ((u.abs() + eu) * (eg + size * (ev + 2.0 ** -22)) + s.abs() * eu)
     edu = h * (1.13 * eg + a.abs() * (ev + 2.0 ** -23))
     dg, du = dH * u * s, dH * a
-    edg = edg + r * (dg.abs() + edg) + t
-    edu = edu + r * (du.abs() + edu) + t
+    edg = edg + rd * (dg.abs() + edg) + t
+    edu = edu + rd * (du.abs() + edu) + t
     M, F = dH.shape
 
     def close(err, mag, n):

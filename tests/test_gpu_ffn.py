@@ -182,7 +182,8 @@ def test_glu_backward_whole_numbers(dev, shape, dtype, layout):
 
 @pytest.mark.parametrize("act", ref.ACTS[:3])
 @pytest.mark.parametrize("dtype", ref.DTYPES)
-@pytest.mark.parametrize("shape", [(1, 64, 256), (9, 130, 77), (200, 150, 300)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 64, 256), (1, 3620, 87), (9, 130, 77), (128, 128, 40), (129, 128, 40),
+                                   (200, 150, 300)], ids=str)
 def test_glu_backward_random(dev, shape, dtype, act):
     M, F, K = shape
     t = ref.DTYPES[dtype]
