@@ -531,6 +531,13 @@ struct DmaCore {
     }
 };
 
+// Waits until this wave's LDS reads are done; nothing moves across. Before a
+// stage that they read is filled again.
+__device__ __forceinline__ void lds_wait() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+    asm volatile("" ::: "memory");
+}
 // Waits until at most VMCNT of this wave's vector-memory operations are
 // outstanding (their LDS writes included); nothing moves across.
 template <int VMCNT>

@@ -144,6 +144,7 @@ __global__ __launch_bounds__(KW * 64) void k_glu_rows(GluArgs a) {
             int at = 0;
             for (int i = 0; i < count; ++i) {
                 const int to = at == 0 ? STAGES - 1 : at - 1;   // the stage read one slice ago
+                lds_wait();
                 issue(i + STAGES - 1, ring + to * STAGE);
                 wave_wait<(STAGES - 1) * (decltype(fa)::G + decltype(fb)::G)>();
                 compute(ring + at * STAGE);

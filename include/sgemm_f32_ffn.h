@@ -25,9 +25,15 @@
  * output and gradient of a call: FP32, bfloat16 or IEEE half. Products are
  * exact and sums are held in FP32 whatever the type; outputs are rounded
  * once. Where a 16-bit call has to keep a value between two products (dG and
- * dU, which the matrix cores read in the type), it is rounded once more. G
- * and U are kept for the backward pass in FP32 (`P`), so that no rounding
- * comes before the derivative.
+ * dU, which the matrix cores read in the type), it is rounded once more, or,
+ * where M * F <= 16384, kept in two parts. G and U are kept for the backward
+ * pass in FP32 (`P`), so that no rounding comes before the derivative.
+ *
+ * Infinities and NaN stay in the rows and columns whose sums they enter. With
+ * 4-bit weights an infinity in X, or a value beyond 2^120 in magnitude, may give
+ * NaN where the exact sum is finite or infinite (the numbers are summed before their
+ * zero point is taken off), and parts of FP32 values below 2^-126 count as
+ * zero.
  *
  * Layout. Every matrix is row-major with unit column stride and a leading
  * dimension in elements (element (r, c) at base[r * ld + c]); a weight has one

@@ -280,6 +280,8 @@ def test_w4_quantize(dev, pack, dtype, zeros):
     W = _normal((F, K), gen, dev, t)
     W[0] = 0                                   # a row of zeros: scale 0
     W[-1] = W[-1].abs()                        # one sign only
+    if F > 4:
+        W[4] = (W[4].double() * (2e-40 if dtype == "f32" else 1e-6)).to(t)    # scales next to 0, or 0
     if F > 3:
         W[1] = _ints((K,), gen, -7, 7, dev, t) * 0.5      # quotients on whole and half steps
         W[2, K // 2] = float("inf")
