@@ -179,7 +179,10 @@ struct W4Groups {
 // reads a row's 1 KiB in one piece, and a group's scale one element per lane, next
 // to its neighbours'. The lane's activations stay in registers while it walks the
 // rows. All of a wave's loads go out before its first product: with a
-// launch that fills the chip once there is no loop to overlap them in.
+// launch that fills the chip once there is no loop to overlap them in. Bound
+// by the weights' bytes and, close behind, by issue: about 60 vector
+// instructions a lane for 32 weights. 8192 x 8192 from HBM, one row: bf16
+// 10.5 us (3.3 TB/s, launch included), FP32 14.4; two rows bf16 13.2.
 // ---------------------------------------------------------------------------
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -387,7 +390,9 @@ static hipError_t launch_few(const W4Args& a, const W4Groups& gr, hipStream_t s)
 // four times as long. A weight row's words reach their step's lanes by a 4 x 4
 // transpose between words and quarters of the wave, which puts 32
 // consecutive k in each step, so any group of whole steps is scaled apart: PER
-// steps of a run share their scales.
+// steps of a run share their scales. Bound by issue: unpacking, and for FP32
+// splitting X, on eight waves a compute unit. 8192 x 8192 from HBM: 16 rows bf16
+// 17.7 us, FP32 (groups of 64, zero points) 27.9; 64 rows bf16 35.1.
 // ---------------------------------------------------------------------------
 
 // The 4 x 4 transpose between a lane's four words and the four quarters of
