@@ -602,8 +602,14 @@ static hipError_t launch_any(const W4Args& a, const W4Groups& gr, hipStream_t s)
     if (a.M <= 2)
         return a.M <= 1 ? launch_few<T, DUAL, 1>(a, gr, s) : launch_few<T, DUAL, 2>(a, gr, s);
     if constexpr (sizeof(T) == 2) {   // (FP32's three parts leave LDS for 16 rows)
-        if (a.M > 32) return launch_rows<T, DUAL, 4, PER>(a, gr, s);
-        if (a.M > 16) return launch_rows<T, DUAL, 2, PER>(a, gr, s);
+        // As few workgroups of up to 64 rows as hold X, of equal height.
+        const int64_t blocks = cdiv(a.M, 64);
+        switch ((int)cdiv(a.M, 16 * blocks)) {
+            case 2: return launch_rows<T, DUAL, 2, PER>(a, gr, s);
+            case 3: return launch_rows<T, DUAL, 3, PER>(a, gr, s);
+            case 4: return launch_rows<T, DUAL, 4, PER>(a, gr, s);
+            default: break;
+        }
     }
     return launch_rows<T, DUAL, 1, PER>(a, gr, s);
 }
