@@ -183,8 +183,18 @@ def _call(like, stream, entry: str, *args) -> None:
         raise SgemmError(rc, entry)
 
 
-def _new(like, rows: int, cols: int):
-    return like.new_empty((rows, cols))
+def _kept(t, stream):
+    """`t`, allocated on the current stream, for work on `stream`: its memory is
+    not handed on before that work is done."""
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        t.record_stream(stream)
+    return t
+
+
+def _new(like, rows: int, cols: int, stream=None):
+    return _kept(like.new_empty((rows, cols)), stream)
 
 
 def glu(X, Wg, Wu, act: str = "silu", out=None, preact=None, stream=None):
@@ -193,7 +203,7 @@ def glu(X, Wg, Wu, act: str = "silu", out=None, preact=None, stream=None):
     d = _gpu(X, "X")
     M, K = X.shape
     F = Wg.shape[0]
-    H = _new(X, M, F) if out is None else out
+    H = _new(X, M, F, stream) if out is None else out
     t = X.dtype
     ldp = 2 * F
     if preact is not None:
@@ -220,12 +230,12 @@ def glu_backward(dH, X, Wg, Wu, preact, act: str = "silu", dX=None, dWg=None, dW
             got.append(None)
             args += [None, max(K, 1)]
         else:
-            g = _new(X, rows, K) if g is None else g
+            g = _new(X, rows, K, stream) if g is None else g
             got.append(g)
             args += [g.data_ptr(), _ld(g, X, t, rows, K, name)]
     need = glu_backward_workspace(X, F)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = _kept(torch.empty(need, dtype=torch.uint8, device=X.device), stream)
     elif workspace.device != X.device:
         raise ValueError(f"workspace is on {workspace.device}, not on {X.device}")
     elif not workspace.is_contiguous():
@@ -275,9 +285,9 @@ def w4_quantize(W, group: int = 128, zeros: bool = False, stream=None) -> W4:
     d = _gpu(W, "W")
     F, K = W.shape
     G = _groups(K, group)
-    q = torch.empty((F, (K + 1) // 2), dtype=torch.uint8, device=W.device)
-    s = _new(W, F, G)
-    z = _new(W, F, G) if zeros else None
+    q = _kept(torch.empty((F, (K + 1) // 2), dtype=torch.uint8, device=W.device), stream)
+    s = _new(W, F, G, stream)
+    z = _new(W, F, G, stream) if zeros else None
     _call(W, stream, "sgemm_f32_w4_quantize", d, F, K, group, W.data_ptr(), _ld(W, W, W.dtype, F, K, "W"),
           q.data_ptr(), max((K + 1) // 2, 1), s.data_ptr(), max(G, 1), z.data_ptr() if zeros else None, max(G, 1))
     return W4(q, s, z, K, group)
@@ -287,7 +297,7 @@ def w4_dequantize(w: W4, out=None, stream=None):
     """The matrix (F, K) that `w` stands for, in the type of its scales."""
     d = _gpu(w.scales, "scales")
     F, q, s, z = _w4(w, w.scales, "w")
-    out = _new(w.scales, F, w.K) if out is None else out
+    out = _new(w.scales, F, w.K, stream) if out is None else out
     _call(w.scales, stream, "sgemm_f32_w4_dequantize", d, F, w.K, w.group, *q, *s, *z, out.data_ptr(),
           _ld(out, w.scales, w.scales.dtype, F, w.K, "out"))
     return out
@@ -298,7 +308,7 @@ def w4_matmul(X, w: W4, out=None, stream=None):
     d = _gpu(X, "X")
     M = X.shape[0]
     F, q, s, z = _w4(w, X, "w")
-    Y = _new(X, M, F) if out is None else out
+    Y = _new(X, M, F, stream) if out is None else out
     _call(X, stream, "sgemm_f32_w4", d, M, F, w.K, w.group, X.data_ptr(), _ld(X, X, X.dtype, M, w.K, "X"),
           *q, *s, *z, Y.data_ptr(), _ld(Y, X, X.dtype, M, F, "out"))
     return Y
@@ -315,7 +325,7 @@ def w4_glu(X, wg: W4, wu: W4, act: str = "silu", out=None, stream=None):
         raise ValueError("wg and wu must have the same shape and group, and both or neither zero points")
     if qg[1] != qu[1] or sg[1] != su[1] or zg[1] != zu[1]:
         raise ValueError("wg and wu must have the same row strides")
-    H = _new(X, M, F) if out is None else out
+    H = _new(X, M, F, stream) if out is None else out
     _call(X, stream, "sgemm_f32_w4_glu", d, _act(act), M, F, wg.K, wg.group, X.data_ptr(),
           _ld(X, X, X.dtype, M, wg.K, "X"), qg[0], qu[0], qg[1], sg[0], su[0], sg[1], zg[0], zu[0], zg[1],
           H.data_ptr(), _ld(H, X, X.dtype, M, F, "out"))

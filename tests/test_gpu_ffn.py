@@ -491,3 +491,65 @@ def test_two_streams(dev):
     torch.cuda.synchronize()
     for a, o in zip(alone, outs):
         assert all(torch.equal(x, y) for x, y in zip(a, o))
+
+
+def test_another_stream_without_workspace(dev):
+    # Outputs and workspace allocated inside the call, which runs on a stream
+    # of its own: the current stream's later allocations must not take them.
+    _say("another stream")
+    gen = _gen(15)
+    X, dH = _normal((500, 300), gen, dev, torch.float16), _normal((500, 400), gen, dev, torch.float16)
+    Wg, Wu = (_normal((400, 300), gen, dev, torch.float16, 0.1) for _ in range(2))
+    P = torch.empty(500, 800, device=dev)
+    sg.glu(X, Wg, Wu, preact=P)
+    alone = sg.glu_backward(dH, X, Wg, Wu, P)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(dev)
+    for stream in (s, s.cuda_stream):
+        for _ in range(3):
+            got = sg.glu_backward(dH, X, Wg, Wu, P, stream=stream)
+            junk = [torch.full((1 << 21,), float("nan"), dtype=torch.float16, device=dev) for _ in range(4)]
+            w = sg.w4_quantize(Wg, 64, stream=stream)
+            y = sg.w4_matmul(X, w, stream=stream)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, alone))
+            assert torch.equal(y, sg.w4_matmul(X, sg.w4_quantize(Wg, 64)))
+            del junk
+
+
+def test_offsets_past_32_bits(dev):
+    # Rows 256 MiB apart: offsets within one operand reach 10 GiB.
+    M, F, K, S = 33, 40, 64, 1 << 27
+    t = torch.bfloat16
+    _say("far rows")
+    big = torch.empty(F * S, dtype=t, device=dev)
+    place = [0]
+
+    def far(rows, cols, dtype=t):
+        per = torch.empty(0, dtype=dtype).element_size() // 2
+        v = big.view(dtype).as_strided((rows, cols), (S // per, 1), place[0] // per)
+        place[0] += (cols * per + 63) // 64 * 64
+        return v
+
+    gen = _gen(16)
+    near = [_ints(s, gen, -2, 2, dev, t) for s in ((M, K), (F, K), (F, K), (M, F))]
+    X, Wg, Wu, dH = (far(*v.shape).copy_(v) for v in near)
+    H, dX, dWg, dWu = far(M, F), far(M, K), far(F, K), far(F, K)
+    P = far(M, 2 * F, torch.float32)
+    sg.glu(X, Wg, Wu, "relu", out=H, preact=P)
+    sg.glu_backward(dH, X, Wg, Wu, P, "relu", dX, dWg, dWu)
+    p = torch.empty(M, 2 * F, device=dev)
+    assert torch.equal(H, sg.glu(near[0], near[1], near[2], "relu", preact=p)) and torch.equal(P, p)
+    for a, b in zip((dX, dWg, dWu), sg.glu_backward(near[3], near[0], near[1], near[2], p, "relu")):
+        assert torch.equal(a, b)
+    q = big.view(torch.uint8).as_strided((F, K // 2), (2 * S, 1), 2 * place[0])
+    place[0] += 64
+    w = sg.w4_quantize(Wg, 32)
+    q.copy_(w.q)
+    for rows in (1, M):
+        y = far(rows, F)
+        sg.w4_matmul(X[:rows], sg.W4(q, w.scales, None, K, 32), out=y)
+        assert torch.equal(y, sg.w4_matmul(near[0][:rows], w))
+    back = far(F, K)
+    sg.w4_dequantize(sg.W4(q, w.scales, None, K, 32), out=back)
+    assert torch.equal(back, sg.w4_dequantize(w))
