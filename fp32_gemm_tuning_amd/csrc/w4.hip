@@ -411,7 +411,10 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
     using C = W4Type<T>;
     constexpr int ROWS = 16 * MB, UNITS = 64 * ROWS;   // 16-byte units of a part's pass
     constexpr int XI = ROWS / 8;                       // units per thread
-    __shared__ i32x4 xs[2][C::PARTS * UNITS];
+    // Two stages of X, or one where two do not fit: the next pass is then
+    // stored behind a barrier of its own.
+    constexpr int STAGES = 2 * C::PARTS * UNITS * 16 <= 128 * 1024 ? 2 : 1;
+    __shared__ i32x4 xs[STAGES][C::PARTS * UNITS];
     __shared__ i32x4 ws[8][64];
     __shared__ float sc[2][2][32][17];   // [stage][scale, 16 + zero point][row][step]
     const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
@@ -469,7 +472,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
     };
     auto store_x = [&](int p, XPass& x) {
         const int k = 512 * p + 8 * lane;
-        i32x4* st = xs[p & 1];
+        i32x4* st = xs[p % STAGES];
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
             const int r = w + 8 * i;
@@ -504,7 +507,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
         ws[w][wl * 4 + ((lane & 3) ^ ((wl >> 1) & 3))] = d;
         d = ws[w][c * 4 + (q ^ ((c >> 1) & 3))];
         transpose4(d);
-        const i32x4* st = xs[p & 1];
+        const i32x4* st = xs[p % STAGES];
         f32x4 part[MB], sx[MB];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -549,6 +552,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
         auto pass = [&](int p, Ahead& now, const Ahead& next, XPass& x) {
             compute(p, now);
             load_ahead(p + 2, now);
+            if constexpr (STAGES == 1) ring_barrier<63>();
             store_x(p + 1, x);
             store_scales(p + 1, next);
             load_x(p + 3, x);
@@ -601,15 +605,15 @@ static hipError_t launch_any(const W4Args& a, const W4Groups& gr, hipStream_t s)
     // would be level).
     if (a.M <= 2)
         return a.M <= 1 ? launch_few<T, DUAL, 1>(a, gr, s) : launch_few<T, DUAL, 2>(a, gr, s);
-    if constexpr (sizeof(T) == 2) {   // (FP32's three parts leave LDS for 16 rows)
-        // As few workgroups of up to 64 rows as hold X, of equal height.
-        const int64_t blocks = cdiv(a.M, 64);
-        switch ((int)cdiv(a.M, 16 * blocks)) {
-            case 2: return launch_rows<T, DUAL, 2, PER>(a, gr, s);
-            case 3: return launch_rows<T, DUAL, 3, PER>(a, gr, s);
-            case 4: return launch_rows<T, DUAL, 4, PER>(a, gr, s);
-            default: break;
-        }
+    // As few workgroups of up to 64 rows (FP32, whose X takes three parts of
+    // LDS: 32) as hold X, of equal height.
+    constexpr int MOST = sizeof(T) == 4 ? 32 : 64;
+    const int64_t blocks = cdiv(a.M, MOST);
+    const int height = (int)cdiv(a.M, 16 * blocks);
+    if (height == 2) return launch_rows<T, DUAL, 2, PER>(a, gr, s);
+    if constexpr (sizeof(T) == 2) {
+        if (height == 3) return launch_rows<T, DUAL, 3, PER>(a, gr, s);
+        if (height == 4) return launch_rows<T, DUAL, 4, PER>(a, gr, s);
     }
     return launch_rows<T, DUAL, 1, PER>(a, gr, s);
 }
