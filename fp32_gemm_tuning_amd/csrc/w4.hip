@@ -379,9 +379,9 @@ static hipError_t launch_few(const W4Args& a, const W4Groups& gr, hipStream_t s)
 // ---------------------------------------------------------------------------
 // More rows: matrix cores.
 //
-// A workgroup's eight waves are two streams of 16 weight rows (32 features, or
-// the two matrices' rows of 16 features) by four runs of 128 k, so one pass of its loop
-// covers 512 k. X's part of a pass is staged in LDS once for both streams,
+// A workgroup's NW waves are two streams of 16 weight rows (32 features, or
+// the two matrices' rows of 16 features) by NW / 2 runs of 128 k, so one pass of
+// its loop covers 64 NW k. X's part of a pass is staged in LDS once for both streams,
 // already paired (and split, for FP32), as 16-byte units [part][k / 8][row],
 // the operand of lane (k / 8 % 4, row) of the 16x16x32 matrix instruction.
 // Memory is read along the rows, consecutive lanes on consecutive 16 bytes, and
@@ -391,8 +391,8 @@ static hipError_t launch_few(const W4Args& a, const W4Groups& gr, hipStream_t s)
 // transpose between words and quarters of the wave, which puts 32
 // consecutive k in each step, so any group of whole steps is scaled apart: PER
 // steps of a run share their scales. Bound by issue: unpacking, and for FP32
-// splitting X, on eight waves a compute unit. 8192 x 8192 from HBM: 16 rows bf16
-// 17.7 us, FP32 (groups of 64, zero points) 27.9; 64 rows bf16 35.1.
+// splitting X, on eight or sixteen waves a compute unit. 8192 x 8192 from HBM: 16
+// rows bf16 16.2 us, FP32 (groups of 64, zero points) 28; 64 rows bf16 34.
 // ---------------------------------------------------------------------------
 
 // The 4 x 4 transpose between a lane's four words and the four quarters of
@@ -406,22 +406,24 @@ __device__ __forceinline__ void transpose4(i32x4& d) {
 }
 
 // SHORT: K < 32, rows too short for whole loads.
-template <class T, bool DUAL, int MB, int PER, bool SHORT = false>
-__global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
+template <class T, bool DUAL, int MB, int PER, int NW, bool SHORT = false>
+__global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
     using C = W4Type<T>;
-    constexpr int ROWS = 16 * MB, UNITS = 64 * ROWS;   // 16-byte units of a part's pass
-    constexpr int XI = ROWS / 8;                       // units per thread
+    constexpr int RUNS = NW / 2, PASS = 128 * RUNS, STEPS = PASS / 32;
+    constexpr int ROWS = 16 * MB, UNITS = PASS / 8 * ROWS;   // 16-byte units of a part's pass
+    constexpr int PIECES = PASS / 512;                       // of 64 units, in a row's pass
+    constexpr int XI = ROWS * PIECES / NW;                   // units per thread
     // Two stages of X, or one where two do not fit: the next pass is then
     // stored behind a barrier of its own.
     constexpr int STAGES = 2 * C::PARTS * UNITS * 16 <= 128 * 1024 ? 2 : 1;
     __shared__ i32x4 xs[STAGES][C::PARTS * UNITS];
-    __shared__ i32x4 ws[8][64];
-    __shared__ float sc[2][2][32][17];   // [stage][scale, 16 + zero point][row][step]
+    __shared__ i32x4 ws[NW][64];
+    __shared__ float sc[2][2][32][STEPS + 1];   // [stage][scale, 16 + zero point][row][step]
     const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
     const int q = lane >> 4, c = lane & 15;
     const int stream = w & 1, run = w >> 1;
     const int f0 = blockIdx.x * (DUAL ? 16 : 32), m0 = blockIdx.y * ROWS;
-    const int bytes = (a.K + 1) / 2, passes = (a.K + 511) / 512;
+    const int bytes = (a.K + 1) / 2, passes = (a.K + PASS - 1) / PASS;
     const bool zeros = a.Z[0] != nullptr;
 
     // What this thread loads: its weight row (of its stream), its scale's row
@@ -431,7 +433,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
     auto clampf = [&](int f) { return (int64_t)(f < a.F ? f : a.F - 1); };
     const int wr = 16 * stream + (lane >> 2);
     const uint8_t* wrow = a.Q[DUAL ? stream : 0] + clampf(feature(wr)) * a.ldq;
-    const int sr = t >> 4, ss = t & 15;
+    const int sr = t / STEPS, ss = t % STEPS;
     const int sd = matrix(sr);
     const T* srow = (const T*)(sd ? a.S[1] : a.S[0]) + clampf(feature(sr)) * a.lds;
     // (without zero points the scale is read again and ignored)
@@ -443,7 +445,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
         T s, z;
     };
     auto load_ahead = [&](int p, Ahead& r) {
-        const int at = 256 * p + 64 * run + 16 * (lane & 3);
+        const int at = PASS / 2 * p + 64 * run + 16 * (lane & 3);
         if constexpr (!SHORT) {
             r.w = load_w32(wrow, at, bytes);
         } else {
@@ -451,7 +453,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
             for (int i = 0; at + i < bytes; ++i) x |= (unsigned __int128)wrow[at + i] << (8 * i);
             r.w = __builtin_bit_cast(i32x4, x);
         }
-        const int st = 16 * p + ss, g = gr.of(st < last_step ? st : last_step);
+        const int st = STEPS * p + ss, g = gr.of(st < last_step ? st : last_step);
         r.s = srow[g];
         r.z = zrow[g];
     };
@@ -459,10 +461,9 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
         XRaw<T> r[XI];
     };
     auto load_x = [&](int p, XPass& x) {
-        const int k = 512 * p + 8 * lane;
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
-            const int m = m0 + w + 8 * i;
+            const int item = w + NW * i, m = m0 + item / PIECES, k = PASS * p + 512 * (item % PIECES) + 8 * lane;
             const T* row = (const T*)a.X + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
             if constexpr (SHORT)
                 x.r[i].fetch_short(row, k, a.K);
@@ -471,16 +472,16 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
         }
     };
     auto store_x = [&](int p, XPass& x) {
-        const int k = 512 * p + 8 * lane;
         i32x4* st = xs[p % STAGES];
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
-            const int r = w + 8 * i;
-            if (!SHORT && 512 * p + 512 > a.K) x.r[i].place(k, a.K);
+            const int item = w + NW * i, r = item / PIECES, k8 = 64 * (item % PIECES) + lane;
+            const int k = PASS * p + 8 * k8;
+            if (!SHORT && PASS * p + PASS > a.K) x.r[i].place(k, a.K);
             i32x4 parts[C::PARTS];
             pair_up(x.r[i], parts);
 #pragma unroll
-            for (int e = 0; e < C::PARTS; ++e) st[e * UNITS + lane * ROWS + (r ^ (lane & 15))] = parts[e];
+            for (int e = 0; e < C::PARTS; ++e) st[e * UNITS + k8 * ROWS + (r ^ (k8 & 15))] = parts[e];
         }
     };
     auto store_scales = [&](int p, const Ahead& r) {
@@ -496,7 +497,7 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
     for (int i = 0; i < MB; ++i) acc[i] = none;
 
     auto compute = [&](int p, const Ahead& r) {
-        const int k0 = 512 * p + 128 * run;
+        const int k0 = PASS * p + 128 * run;
         if (k0 >= a.K) return;
         i32x4 d = r.w;
         if (!SHORT && k0 + 128 > a.K) d = place_w32(d, (k0 >> 1) + 16 * (lane & 3), bytes);
@@ -571,13 +572,13 @@ __global__ __launch_bounds__(512) void k_w4_rows(W4Args a, W4Groups gr) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) red[((w * MB + i) * 4 + e) * 68 + lane] = acc[i][e];
     __syncthreads();
-    for (int o = t; o < MB * 256 * (DUAL ? 1 : 2); o += 512) {
+    for (int o = t; o < MB * 256 * (DUAL ? 1 : 2); o += NW * 64) {
         const int i = (o >> 4) / (DUAL ? 16 : 32), f = DUAL ? o & 15 : o & 31, row = (o / (DUAL ? 16 : 32)) & 15;
         float v[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int d = 0; d < (DUAL ? 2 : 1); ++d)
 #pragma unroll
-            for (int rn = 0; rn < 4; ++rn) {
+            for (int rn = 0; rn < RUNS; ++rn) {
                 const int ww = 2 * rn + (DUAL ? d : f >> 4);
                 v[d] += red[((ww * MB + i) * 4 + (row & 3)) * 68 + (row >> 2) * 16 + (f & 15)];
             }
@@ -591,10 +592,10 @@ int check_w4(const W4Args& a, bool) {
     return cdiv(a.M, 16) <= 65535 && cdiv(a.F, 4) <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
-template <class T, bool DUAL, int MB, int PER, bool SHORT = false>
+template <class T, bool DUAL, int MB, int PER, bool SHORT = false, int NW = 8>
 static hipError_t launch_rows(const W4Args& a, const W4Groups& gr, hipStream_t s) {
     const dim3 grid((unsigned)cdiv(a.F, DUAL ? 16 : 32), (unsigned)cdiv(a.M, 16 * MB));
-    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER, SHORT>), grid, dim3(512), 0, s, a, gr);
+    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER, NW, SHORT>), grid, dim3(NW * 64), 0, s, a, gr);
     return hipGetLastError();
 }
 
@@ -614,6 +615,12 @@ static hipError_t launch_any(const W4Args& a, const W4Groups& gr, hipStream_t s)
     if constexpr (sizeof(T) == 2) {
         if (height == 3) return launch_rows<T, DUAL, 3, PER>(a, gr, s);
         if (height == 4) return launch_rows<T, DUAL, 4, PER>(a, gr, s);
+        // Sixteen waves where a unit holds one workgroup and the rows are long (16
+        // rows bf16: 8192 x 8192 17.9 -> 16.2 us, 4096 x 14336 26.2 -> 21.6;
+        // with two workgroups, gated 8192 x 4096, 14.1 -> 17.7; 3000 k 7.6 -> 7.9).
+        // FP32's X then fits one stage only: level.
+        if (a.K >= 8192 && cdiv(a.F, DUAL ? 16 : 32) <= 256)
+            return launch_rows<T, DUAL, 1, PER, false, 16>(a, gr, s);
     }
     return launch_rows<T, DUAL, 1, PER>(a, gr, s);
 }
