@@ -406,56 +406,67 @@ __device__ __forceinline__ void transpose4(i32x4& d) {
 }
 
 // SHORT: K < 32, rows too short for whole loads.
-template <class T, bool DUAL, int MB, int PER, int NW, bool SHORT = false>
+template <class T, bool DUAL, int MB, int PER, int NW, int NB, bool SHORT>
 __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
     using C = W4Type<T>;
     constexpr int RUNS = NW / 2, PASS = 128 * RUNS, STEPS = PASS / 32;
     constexpr int ROWS = 16 * MB, UNITS = PASS / 8 * ROWS;   // 16-byte units of a part's pass
     constexpr int PIECES = PASS / 512;                       // of 64 units, in a row's pass
     constexpr int XI = ROWS * PIECES / NW;                   // units per thread
+    constexpr int HALF = 16 * NB, OUTS = DUAL ? HALF : 2 * HALF;   // weight rows of a stream; outputs
     // Two stages of X, or one where two do not fit: the next pass is then
     // stored behind a barrier of its own.
     constexpr int STAGES = 2 * C::PARTS * UNITS * 16 <= 128 * 1024 ? 2 : 1;
     __shared__ i32x4 xs[STAGES][C::PARTS * UNITS];
     __shared__ i32x4 ws[NW][64];
-    __shared__ float sc[2][2][32][STEPS + 1];   // [stage][scale, 16 + zero point][row][step]
+    __shared__ float sc[2][2][2 * HALF][STEPS + 1];   // [stage][scale, 16 + zero point][row][step]
     const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
     const int q = lane >> 4, c = lane & 15;
     const int stream = w & 1, run = w >> 1;
-    const int f0 = blockIdx.x * (DUAL ? 16 : 32), m0 = blockIdx.y * ROWS;
+    const int f0 = blockIdx.x * OUTS, m0 = blockIdx.y * ROWS;
     const int bytes = (a.K + 1) / 2, passes = (a.K + PASS - 1) / PASS;
     const bool zeros = a.Z[0] != nullptr;
 
-    // What this thread loads: its weight row (of its stream), its scale's row
+    // What this thread loads: its weight rows (of its stream), its scales' rows
     // and its rows of X. Rows past the last repeat it; their results are not stored.
-    auto feature = [&](int r) { return DUAL ? f0 + (r & 15) : f0 + r; };   // of row r of 32
-    auto matrix = [&](int r) { return DUAL ? r >> 4 : 0; };
-    auto clampf = [&](int f) { return (int64_t)(f < a.F ? f : a.F - 1); };
-    const int wr = 16 * stream + (lane >> 2);
-    const uint8_t* wrow = a.Q[DUAL ? stream : 0] + clampf(feature(wr)) * a.ldq;
-    const int sr = t / STEPS, ss = t % STEPS;
-    const int sd = matrix(sr);
-    const T* srow = (const T*)(sd ? a.S[1] : a.S[0]) + clampf(feature(sr)) * a.lds;
-    // (without zero points the scale is read again and ignored)
-    const T* zrow = zeros ? (const T*)(sd ? a.Z[1] : a.Z[0]) + clampf(feature(sr)) * a.ldz : srow;
+    auto feature = [&](int r) {   // of row r of 2 HALF
+        const int f = DUAL ? f0 + r % HALF : f0 + r;
+        return (int64_t)(f < a.F ? f : a.F - 1);
+    };
+    const uint8_t* wrow[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        wrow[b] = a.Q[DUAL ? stream : 0] + feature(HALF * stream + 16 * b + (lane >> 2)) * a.ldq;
+    const int sr = t / STEPS, ss = t % STEPS;   // (and rows 32 further for each b)
+    const T *srow[NB], *zrow[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int r = sr + 32 * b, m = DUAL ? r / HALF : 0;
+        srow[b] = (const T*)(m ? a.S[1] : a.S[0]) + feature(r) * a.lds;
+        // (without zero points the scale is read again and ignored)
+        zrow[b] = zeros ? (const T*)(m ? a.Z[1] : a.Z[0]) + feature(r) * a.ldz : srow[b];
+    }
     const int last_step = (a.K - 1) >> 5;
 
     struct Ahead {   // one pass's weights and scales, on their way
-        i32x4 w;
-        T s, z;
+        i32x4 w[NB];
+        T s[NB], z[NB];
     };
     auto load_ahead = [&](int p, Ahead& r) {
         const int at = PASS / 2 * p + 64 * run + 16 * (lane & 3);
-        if constexpr (!SHORT) {
-            r.w = load_w32(wrow, at, bytes);
-        } else {
-            unsigned __int128 x = 0;
-            for (int i = 0; at + i < bytes; ++i) x |= (unsigned __int128)wrow[at + i] << (8 * i);
-            r.w = __builtin_bit_cast(i32x4, x);
-        }
         const int st = STEPS * p + ss, g = gr.of(st < last_step ? st : last_step);
-        r.s = srow[g];
-        r.z = zrow[g];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if constexpr (!SHORT) {
+                r.w[b] = load_w32(wrow[b], at, bytes);
+            } else {
+                unsigned __int128 x = 0;
+                for (int i = 0; at + i < bytes; ++i) x |= (unsigned __int128)wrow[b][at + i] << (8 * i);
+                r.w[b] = __builtin_bit_cast(i32x4, x);
+            }
+            r.s[b] = srow[b][g];
+            r.z[b] = zrow[b][g];
+        }
     };
     struct XPass {
         XRaw<T> r[XI];
@@ -485,70 +496,92 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
         }
     };
     auto store_scales = [&](int p, const Ahead& r) {
-        sc[p & 1][0][sr][ss] = (float)r.s;
-        sc[p & 1][1][sr][ss] = 16.0f + (zeros ? (float)r.z : 8.0f);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            sc[p & 1][0][sr + 32 * b][ss] = (float)r.s[b];
+            sc[p & 1][1][sr + 32 * b][ss] = 16.0f + (zeros ? (float)r.z[b] : 8.0f);
+        }
     };
 
     const Unpack<T> unpack;
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
     const i32x4 ones = {(int)C::ONES, (int)C::ONES, (int)C::ONES, (int)C::ONES};
-    f32x4 acc[MB];
+    f32x4 acc[NB][MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) acc[i] = none;
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) acc[b][i] = none;
 
     auto compute = [&](int p, const Ahead& r) {
         const int k0 = PASS * p + 128 * run;
         if (k0 >= a.K) return;
-        i32x4 d = r.w;
-        if (!SHORT && k0 + 128 > a.K) d = place_w32(d, (k0 >> 1) + 16 * (lane & 3), bytes);
-        // Rows to operand order: unit (row, chunk) at chunk ^ (row / 2 % 4) of
-        // its row, so that both accesses spread over all banks. A wave's
-        // own units only: no barrier.
-        const int wl = lane >> 2;
-        ws[w][wl * 4 + ((lane & 3) ^ ((wl >> 1) & 3))] = d;
-        d = ws[w][c * 4 + (q ^ ((c >> 1) & 3))];
-        transpose4(d);
+        i32x4 d[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            d[b] = r.w[b];
+            if (!SHORT && k0 + 128 > a.K) d[b] = place_w32(d[b], (k0 >> 1) + 16 * (lane & 3), bytes);
+            // Rows to operand order: unit (row, chunk) at chunk ^ (row / 2 % 4) of
+            // its row, so that both accesses spread over all banks. A wave's
+            // own units only: no barrier.
+            const int wl = lane >> 2;
+            ws[w][wl * 4 + ((lane & 3) ^ ((wl >> 1) & 3))] = d[b];
+            d[b] = ws[w][c * 4 + (q ^ ((c >> 1) & 3))];
+            transpose4(d[b]);
+        }
         const i32x4* st = xs[p % STAGES];
-        f32x4 part[MB], sx[MB];
+        f32x4 part[NB][MB], sx[MB];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (k0 + 32 * j >= a.K) break;
-            const i32x4 u = unpack((uint32_t)d[j]);
+            i32x4 u[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) u[b] = unpack((uint32_t)d[b][j]);
             const int k8 = 16 * run + 4 * j + q;
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
-                if (j % PER == 0) part[i] = sx[i] = none;
+                if (j % PER == 0) {
+                    sx[i] = none;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) part[b][i] = none;
+                }
 #pragma unroll
                 for (int e = 0; e < C::PARTS; ++e) {
                     const i32x4 x = st[e * UNITS + k8 * ROWS + ((16 * i + c) ^ (k8 & 15))];
-                    part[i] = C::mma(x, u, part[i]);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) part[b][i] = C::mma(x, u[b], part[b][i]);
                     sx[i] = C::mma(x, ones, sx[i]);
                 }
             }
             if ((j + 1) % PER == 0 || k0 + 32 * (j + 1) >= a.K) {
                 const int at = 4 * run + j / PER * PER;
-                const float s = sc[p & 1][0][16 * stream + c][at], z = sc[p & 1][1][16 * stream + c][at];
 #pragma unroll
-                for (int i = 0; i < MB; ++i)
+                for (int b = 0; b < NB; ++b) {
+                    const int row = HALF * stream + 16 * b + c;
+                    const float s = sc[p & 1][0][row][at], z = sc[p & 1][1][row][at];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][e] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[i][e], part[i][e]), acc[i][e]);
+                    for (int i = 0; i < MB; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[b][i][e] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[i][e], part[b][i][e]), acc[b][i][e]);
+                }
             }
         }
     };
 
     if (passes > 0) {
         // Each register set is refilled as soon as it is used, so weights are
-        // two passes ahead and X nearly two; the barrier waits for LDS only.
+        // two passes ahead and X nearly two, or, where registers run out, nearly one;
+        // the barrier waits for LDS only.
+        constexpr bool DEEP = MB * NB < 8;
         Ahead r0, r1;
         XPass x0, x1;
         load_x(0, x0);
         load_ahead(0, r0);
-        load_x(1, x1);
+        if constexpr (DEEP) load_x(1, x1);
         load_ahead(1, r1);
         store_x(0, x0);
         store_scales(0, r0);
-        load_x(2, x0);
+        load_x(DEEP ? 2 : 1, x0);
         ring_barrier<63>();
         auto pass = [&](int p, Ahead& now, const Ahead& next, XPass& x) {
             compute(p, now);
@@ -556,32 +589,34 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
             if constexpr (STAGES == 1) ring_barrier<63>();
             store_x(p + 1, x);
             store_scales(p + 1, next);
-            load_x(p + 3, x);
+            load_x(p + (DEEP ? 3 : 2), x);
             ring_barrier<63>();
         };
         for (int p = 0; p < passes; p += 2) {
-            pass(p, r0, r1, x1);
+            pass(p, r0, r1, DEEP ? x1 : x0);
             if (p + 1 < passes) pass(p + 1, r1, r0, x0);
         }
     }
 
     // Sums over the runs in their order, through the space of X.
     float* red = (float*)xs;
+    static_assert(NW * NB * MB * 4 * 68 * 4 <= (int)sizeof(xs), "the sums fit in the space of X");
+    auto slot = [](int wave, int b, int i, int e) { return (((wave * NB + b) * MB + i) * 4 + e) * 68; };
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) red[((w * MB + i) * 4 + e) * 68 + lane] = acc[i][e];
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[slot(w, b, i, e) + lane] = acc[b][i][e];
     __syncthreads();
-    for (int o = t; o < MB * 256 * (DUAL ? 1 : 2); o += NW * 64) {
-        const int i = (o >> 4) / (DUAL ? 16 : 32), f = DUAL ? o & 15 : o & 31, row = (o / (DUAL ? 16 : 32)) & 15;
+    for (int o = t; o < ROWS * OUTS; o += NW * 64) {
+        const int f = o % OUTS, row = (o / OUTS) & 15, i = o / OUTS / 16;
         float v[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int d = 0; d < (DUAL ? 2 : 1); ++d)
 #pragma unroll
-            for (int rn = 0; rn < RUNS; ++rn) {
-                const int ww = 2 * rn + (DUAL ? d : f >> 4);
-                v[d] += red[((ww * MB + i) * 4 + (row & 3)) * 68 + (row >> 2) * 16 + (f & 15)];
-            }
+            for (int rn = 0; rn < RUNS; ++rn)
+                v[d] += red[slot(2 * rn + (DUAL ? d : f / HALF), f % HALF / 16, i, row & 3) + (row >> 2) * 16 + (f & 15)];
         const int m = m0 + 16 * i + row;
         if (m < a.M && f0 + f < a.F)
             ((T*)a.Y)[(int64_t)m * a.ldy + f0 + f] = (T)(DUAL ? act_value<sizeof(T) == 4>(a.act, v[0]) * v[1] : v[0]);
@@ -592,10 +627,10 @@ int check_w4(const W4Args& a, bool) {
     return cdiv(a.M, 16) <= 65535 && cdiv(a.F, 4) <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
-template <class T, bool DUAL, int MB, int PER, bool SHORT = false, int NW = 8>
+template <class T, bool DUAL, int MB, int PER, int NW = 8, int NB = 1, bool SHORT = false>
 static hipError_t launch_rows(const W4Args& a, const W4Groups& gr, hipStream_t s) {
-    const dim3 grid((unsigned)cdiv(a.F, DUAL ? 16 : 32), (unsigned)cdiv(a.M, 16 * MB));
-    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER, NW, SHORT>), grid, dim3(NW * 64), 0, s, a, gr);
+    const dim3 grid((unsigned)cdiv(a.F, (DUAL ? 16 : 32) * NB), (unsigned)cdiv(a.M, 16 * MB));
+    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER, NW, NB, SHORT>), grid, dim3(NW * 64), 0, s, a, gr);
     return hipGetLastError();
 }
 
@@ -609,18 +644,21 @@ static hipError_t launch_any(const W4Args& a, const W4Groups& gr, hipStream_t s)
     // As few workgroups of up to 64 rows (FP32, whose X takes three parts of
     // LDS: 32) as hold X, of equal height.
     constexpr int MOST = sizeof(T) == 4 ? 32 : 64;
-    const int64_t blocks = cdiv(a.M, MOST);
+    const int64_t blocks = cdiv(a.M, MOST), wide = cdiv(a.F, DUAL ? 32 : 64) * blocks;
     const int height = (int)cdiv(a.M, 16 * blocks);
-    if (height == 2) return launch_rows<T, DUAL, 2, PER>(a, gr, s);
+    const bool twice = wide >= 256;
+    if (height == 2)
+        return twice ? launch_rows<T, DUAL, 2, PER, 8, 2>(a, gr, s) : launch_rows<T, DUAL, 2, PER>(a, gr, s);
     if constexpr (sizeof(T) == 2) {
-        if (height == 3) return launch_rows<T, DUAL, 3, PER>(a, gr, s);
-        if (height == 4) return launch_rows<T, DUAL, 4, PER>(a, gr, s);
+        if (height == 3)
+            return twice ? launch_rows<T, DUAL, 3, PER, 8, 2>(a, gr, s) : launch_rows<T, DUAL, 3, PER>(a, gr, s);
+        if (height == 4)
+            return twice ? launch_rows<T, DUAL, 4, PER, 8, 2>(a, gr, s) : launch_rows<T, DUAL, 4, PER>(a, gr, s);
         // Sixteen waves where a unit holds one workgroup and the rows are long (16
         // rows bf16: 8192 x 8192 17.9 -> 16.2 us, 4096 x 14336 26.2 -> 21.6;
         // with two workgroups, gated 8192 x 4096, 14.1 -> 17.7; 3000 k 7.6 -> 7.9).
         // FP32's X then fits one stage only: level.
-        if (a.K >= 8192 && cdiv(a.F, DUAL ? 16 : 32) <= 256)
-            return launch_rows<T, DUAL, 1, PER, false, 16>(a, gr, s);
+        if (a.K >= 8192 && cdiv(a.F, DUAL ? 16 : 32) <= 256) return launch_rows<T, DUAL, 1, PER, 16>(a, gr, s);
     }
     return launch_rows<T, DUAL, 1, PER>(a, gr, s);
 }
@@ -632,7 +670,7 @@ hipError_t launch_w4(int dtype, const W4Args& a, bool dual, hipStream_t s) {
         using T = typename decltype(tag)::type;
         auto go = [&](auto d) {
             constexpr bool D = decltype(d)::value;
-            if (a.K < 32) return launch_rows<T, D, 1, 1, true>(a, gr, s);
+            if (a.K < 32) return launch_rows<T, D, 1, 1, 8, 1, true>(a, gr, s);
             if (gr.steps % 4 == 0) return launch_any<T, D, 4>(a, gr, s);
             if (gr.steps % 2 == 0) return launch_any<T, D, 2>(a, gr, s);
             return launch_any<T, D, 1>(a, gr, s);
