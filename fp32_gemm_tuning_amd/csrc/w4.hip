@@ -379,9 +379,9 @@ static hipError_t launch_few(const W4Args& a, const W4Groups& gr, hipStream_t s)
 // ---------------------------------------------------------------------------
 // More rows: matrix cores.
 //
-// A workgroup's NW waves are two streams of 16 weight rows (32 features, or
-// the two matrices' rows of 16 features) by NW / 2 runs of 128 k, so one pass of
-// its loop covers 64 NW k. X's part of a pass is staged in LDS once for both streams,
+// A workgroup's NW waves are STREAMS streams of 16 NB weight rows (at the least 32
+// features, or the two matrices' rows of 16 features) by NW / STREAMS runs of 128 k,
+// which one pass of its loop covers. X's part of a pass is staged in LDS once for all streams,
 // already paired (and split, for FP32), as 16-byte units [part][k / 8][row],
 // the operand of lane (k / 8 % 4, row) of the 16x16x32 matrix instruction.
 // Memory is read along the rows, consecutive lanes on consecutive 16 bytes, and
@@ -391,8 +391,10 @@ static hipError_t launch_few(const W4Args& a, const W4Groups& gr, hipStream_t s)
 // transpose between words and quarters of the wave, which puts 32
 // consecutive k in each step, so any group of whole steps is scaled apart: PER
 // steps of a run share their scales. Bound by issue: unpacking, and for FP32
-// splitting X, on eight or sixteen waves a compute unit. 8192 x 8192 from HBM: 16
-// rows bf16 16.2 us, FP32 (groups of 64, zero points) 28; 64 rows bf16 34.
+// splitting X, on eight or sixteen waves a compute unit; with many rows by the loads
+// of X, once for each workgroup's features, and their staging. 8192 x 8192 from
+// HBM: 16 rows bf16 16.2 us, FP32 (groups of 64, zero points) 28; 64 rows bf16 35, FP32
+// 54; 256 rows 71 and 162.
 // ---------------------------------------------------------------------------
 
 // The 4 x 4 transpose between a lane's four words and the four quarters of
@@ -406,42 +408,43 @@ __device__ __forceinline__ void transpose4(i32x4& d) {
 }
 
 // SHORT: K < 32, rows too short for whole loads.
-template <class T, bool DUAL, int MB, int PER, int NW, int NB, bool SHORT>
+template <class T, bool DUAL, int MB, int PER, int NW, int NB, int STREAMS, bool SHORT>
 __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
     using C = W4Type<T>;
-    constexpr int RUNS = NW / 2, PASS = 128 * RUNS, STEPS = PASS / 32;
+    constexpr int RUNS = NW / STREAMS, PASS = 128 * RUNS, STEPS = PASS / 32;
     constexpr int ROWS = 16 * MB, UNITS = PASS / 8 * ROWS;   // 16-byte units of a part's pass
-    constexpr int PIECES = PASS / 512;                       // of 64 units, in a row's pass
-    constexpr int XI = ROWS * PIECES / NW;                   // units per thread
-    constexpr int HALF = 16 * NB, OUTS = DUAL ? HALF : 2 * HALF;   // weight rows of a stream; outputs
+    constexpr int XI = UNITS / (NW * 64);                    // units per thread
+    constexpr int WROWS = 16 * NB * STREAMS, HALF = WROWS / 2;     // weight rows; DUAL: of a matrix
+    constexpr int OUTS = DUAL ? HALF : WROWS;
     // Two stages of X, or one where two do not fit: the next pass is then
     // stored behind a barrier of its own.
     constexpr int STAGES = 2 * C::PARTS * UNITS * 16 <= 128 * 1024 ? 2 : 1;
-    __shared__ i32x4 xs[STAGES][C::PARTS * UNITS];
+    constexpr int SUMS = NW * NB * MB * 4 * 68 / 4;   // units of the sums at the end
+    __shared__ i32x4 xs[STAGES * C::PARTS * UNITS > SUMS ? STAGES * C::PARTS * UNITS : SUMS];
     __shared__ i32x4 ws[NW][64];
-    __shared__ float sc[2][2][2 * HALF][STEPS + 1];   // [stage][scale, 16 + zero point][row][step]
+    __shared__ float sc[2][2][WROWS][STEPS + 1];   // [stage][scale, 16 + zero point][row][step]
     const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
     const int q = lane >> 4, c = lane & 15;
-    const int stream = w & 1, run = w >> 1;
+    const int stream = w % STREAMS, run = w / STREAMS;
     const int f0 = blockIdx.x * OUTS, m0 = blockIdx.y * ROWS;
     const int bytes = (a.K + 1) / 2, passes = (a.K + PASS - 1) / PASS;
     const bool zeros = a.Z[0] != nullptr;
 
     // What this thread loads: its weight rows (of its stream), its scales' rows
     // and its rows of X. Rows past the last repeat it; their results are not stored.
-    auto feature = [&](int r) {   // of row r of 2 HALF
+    auto feature = [&](int r) {   // of weight row r
         const int f = DUAL ? f0 + r % HALF : f0 + r;
         return (int64_t)(f < a.F ? f : a.F - 1);
     };
     const uint8_t* wrow[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-        wrow[b] = a.Q[DUAL ? stream : 0] + feature(HALF * stream + 16 * b + (lane >> 2)) * a.ldq;
-    const int sr = t / STEPS, ss = t % STEPS;   // (and rows 32 further for each b)
+        wrow[b] = a.Q[DUAL ? stream / (STREAMS / 2) : 0] + feature(16 * (NB * stream + b) + (lane >> 2)) * a.ldq;
+    const int sr = t / STEPS, ss = t % STEPS;   // (and 16 STREAMS rows further for each b)
     const T *srow[NB], *zrow[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        const int r = sr + 32 * b, m = DUAL ? r / HALF : 0;
+        const int r = sr + 16 * STREAMS * b, m = DUAL ? r / HALF : 0;
         srow[b] = (const T*)(m ? a.S[1] : a.S[0]) + feature(r) * a.lds;
         // (without zero points the scale is read again and ignored)
         zrow[b] = zeros ? (const T*)(m ? a.Z[1] : a.Z[0]) + feature(r) * a.ldz : srow[b];
@@ -468,13 +471,18 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
             r.z[b] = zrow[b][g];
         }
     };
+    // The row and place of this thread's unit i of X (the row is one a wave where
+    // a row has at least 64 units).
+    constexpr int LINE = PASS / 8;
+    auto x_row = [&](int i) { return LINE >= 64 ? (w + NW * i) / (LINE / 64 > 0 ? LINE / 64 : 1) : (t + NW * 64 * i) / LINE; };
+    auto x_k8 = [&](int i) { return (t + NW * 64 * i) % LINE; };
     struct XPass {
         XRaw<T> r[XI];
     };
     auto load_x = [&](int p, XPass& x) {
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
-            const int item = w + NW * i, m = m0 + item / PIECES, k = PASS * p + 512 * (item % PIECES) + 8 * lane;
+            const int m = m0 + x_row(i), k = PASS * p + 8 * x_k8(i);
             const T* row = (const T*)a.X + (int64_t)(m < a.M ? m : a.M - 1) * a.ldx;
             if constexpr (SHORT)
                 x.r[i].fetch_short(row, k, a.K);
@@ -483,10 +491,10 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
         }
     };
     auto store_x = [&](int p, XPass& x) {
-        i32x4* st = xs[p % STAGES];
+        i32x4* st = xs + p % STAGES * (C::PARTS * UNITS);
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
-            const int item = w + NW * i, r = item / PIECES, k8 = 64 * (item % PIECES) + lane;
+            const int r = x_row(i), k8 = x_k8(i);
             const int k = PASS * p + 8 * k8;
             if (!SHORT && PASS * p + PASS > a.K) x.r[i].place(k, a.K);
             i32x4 parts[C::PARTS];
@@ -498,8 +506,8 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
     auto store_scales = [&](int p, const Ahead& r) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            sc[p & 1][0][sr + 32 * b][ss] = (float)r.s[b];
-            sc[p & 1][1][sr + 32 * b][ss] = 16.0f + (zeros ? (float)r.z[b] : 8.0f);
+            sc[p & 1][0][sr + 16 * STREAMS * b][ss] = (float)r.s[b];
+            sc[p & 1][1][sr + 16 * STREAMS * b][ss] = 16.0f + (zeros ? (float)r.z[b] : 8.0f);
         }
     };
 
@@ -528,7 +536,7 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
             d[b] = ws[w][c * 4 + (q ^ ((c >> 1) & 3))];
             transpose4(d[b]);
         }
-        const i32x4* st = xs[p % STAGES];
+        const i32x4* st = xs + p % STAGES * (C::PARTS * UNITS);
         f32x4 part[NB][MB], sx[MB];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -556,7 +564,7 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
                 const int at = 4 * run + j / PER * PER;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const int row = HALF * stream + 16 * b + c;
+                    const int row = 16 * (NB * stream + b) + c;
                     const float s = sc[p & 1][0][row][at], z = sc[p & 1][1][row][at];
 #pragma unroll
                     for (int i = 0; i < MB; ++i)
@@ -572,7 +580,7 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
         // Each register set is refilled as soon as it is used, so weights are
         // two passes ahead and X nearly two, or, where registers run out, nearly one;
         // the barrier waits for LDS only.
-        constexpr bool DEEP = MB * NB < 8;
+        constexpr bool DEEP = MB * NB < 8 || STREAMS > 2;
         Ahead r0, r1;
         XPass x0, x1;
         load_x(0, x0);
@@ -600,7 +608,6 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
 
     // Sums over the runs in their order, through the space of X.
     float* red = (float*)xs;
-    static_assert(NW * NB * MB * 4 * 68 * 4 <= (int)sizeof(xs), "the sums fit in the space of X");
     auto slot = [](int wave, int b, int i, int e) { return (((wave * NB + b) * MB + i) * 4 + e) * 68; };
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -613,10 +620,12 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
         const int f = o % OUTS, row = (o / OUTS) & 15, i = o / OUTS / 16;
         float v[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int d = 0; d < (DUAL ? 2 : 1); ++d)
+        for (int d = 0; d < (DUAL ? 2 : 1); ++d) {
+            const int wt = (HALF * d + f) / 16;   // the 16 weight rows of this sum
 #pragma unroll
             for (int rn = 0; rn < RUNS; ++rn)
-                v[d] += red[slot(2 * rn + (DUAL ? d : f / HALF), f % HALF / 16, i, row & 3) + (row >> 2) * 16 + (f & 15)];
+                v[d] += red[slot(STREAMS * rn + wt / NB, wt % NB, i, row & 3) + (row >> 2) * 16 + (f & 15)];
+        }
         const int m = m0 + 16 * i + row;
         if (m < a.M && f0 + f < a.F)
             ((T*)a.Y)[(int64_t)m * a.ldy + f0 + f] = (T)(DUAL ? act_value<sizeof(T) == 4>(a.act, v[0]) * v[1] : v[0]);
@@ -627,10 +636,10 @@ int check_w4(const W4Args& a, bool) {
     return cdiv(a.M, 16) <= 65535 && cdiv(a.F, 4) <= max_workgroups(512) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
-template <class T, bool DUAL, int MB, int PER, int NW = 8, int NB = 1, bool SHORT = false>
+template <class T, bool DUAL, int MB, int PER, int NW = 8, int NB = 1, int STREAMS = 2, bool SHORT = false>
 static hipError_t launch_rows(const W4Args& a, const W4Groups& gr, hipStream_t s) {
-    const dim3 grid((unsigned)cdiv(a.F, (DUAL ? 16 : 32) * NB), (unsigned)cdiv(a.M, 16 * MB));
-    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER, NW, NB, SHORT>), grid, dim3(NW * 64), 0, s, a, gr);
+    const dim3 grid((unsigned)cdiv(a.F, (DUAL ? 8 : 16) * NB * STREAMS), (unsigned)cdiv(a.M, 16 * MB));
+    hipLaunchKernelGGL((k_w4_rows<T, DUAL, MB, PER, NW, NB, STREAMS, SHORT>), grid, dim3(NW * 64), 0, s, a, gr);
     return hipGetLastError();
 }
 
@@ -644,16 +653,27 @@ static hipError_t launch_any(const W4Args& a, const W4Groups& gr, hipStream_t s)
     // As few workgroups of up to 64 rows (FP32, whose X takes three parts of
     // LDS: 32) as hold X, of equal height.
     constexpr int MOST = sizeof(T) == 4 ? 32 : 64;
-    const int64_t blocks = cdiv(a.M, MOST), wide = cdiv(a.F, DUAL ? 32 : 64) * blocks;
+    const int64_t blocks = cdiv(a.M, MOST);
     const int height = (int)cdiv(a.M, 16 * blocks);
-    const bool twice = wide >= 256;
-    if (height == 2)
-        return twice ? launch_rows<T, DUAL, 2, PER, 8, 2>(a, gr, s) : launch_rows<T, DUAL, 2, PER>(a, gr, s);
+    // 32, 64 or 128 weight rows a workgroup: X is staged and its fragments are read
+    // once for all of them, but fewer workgroups run. A round of 256 over 8192 k
+    // takes 36, 46 or 71 us (64 rows of X, 16-bit), 47, 55 or 80 (32 rows, FP32),
+    // so by those and the rounds (8192 x 8192, 256 rows: bf16 122, 80, 71, FP32
+    // 322, 195, 162; 4096 rows bf16 1746, 1179, 979).
+    auto rounds = [&](int rows) { return (double)cdiv(cdiv(a.F, DUAL ? rows / 2 : rows) * blocks, 256); };
+    constexpr bool F32 = sizeof(T) == 4;
+    const double by32 = rounds(32) * (F32 ? 47 : 36), by64 = rounds(64) * (F32 ? 55 : 46),
+                 by128 = rounds(128) * (F32 ? 80 : 71);
+    auto many = [&](auto mb) {
+        constexpr int MB = decltype(mb)::value;
+        if (by32 <= by64 && by32 <= by128) return launch_rows<T, DUAL, MB, PER>(a, gr, s);
+        return by64 <= by128 ? launch_rows<T, DUAL, MB, PER, 8, 2>(a, gr, s)
+                             : launch_rows<T, DUAL, MB, PER, 8, 2, 4>(a, gr, s);
+    };
+    if (height == 2) return many(std::integral_constant<int, 2>{});
     if constexpr (sizeof(T) == 2) {
-        if (height == 3)
-            return twice ? launch_rows<T, DUAL, 3, PER, 8, 2>(a, gr, s) : launch_rows<T, DUAL, 3, PER>(a, gr, s);
-        if (height == 4)
-            return twice ? launch_rows<T, DUAL, 4, PER, 8, 2>(a, gr, s) : launch_rows<T, DUAL, 4, PER>(a, gr, s);
+        if (height == 3) return many(std::integral_constant<int, 3>{});
+        if (height == 4) return many(std::integral_constant<int, 4>{});
         // Sixteen waves where a unit holds one workgroup and the rows are long (16
         // rows bf16: 8192 x 8192 17.9 -> 16.2 us, 4096 x 14336 26.2 -> 21.6;
         // with two workgroups, gated 8192 x 4096, 14.1 -> 17.7; 3000 k 7.6 -> 7.9).
@@ -670,7 +690,7 @@ hipError_t launch_w4(int dtype, const W4Args& a, bool dual, hipStream_t s) {
         using T = typename decltype(tag)::type;
         auto go = [&](auto d) {
             constexpr bool D = decltype(d)::value;
-            if (a.K < 32) return launch_rows<T, D, 1, 1, 8, 1, true>(a, gr, s);
+            if (a.K < 32) return launch_rows<T, D, 1, 1, 8, 1, 2, true>(a, gr, s);
             if (gr.steps % 4 == 0) return launch_any<T, D, 4>(a, gr, s);
             if (gr.steps % 2 == 0) return launch_any<T, D, 2>(a, gr, s);
             return launch_any<T, D, 1>(a, gr, s);

@@ -323,7 +323,8 @@ W4_SHAPES = [(1, 1, 1, 32), (1, 48, 256, 32), (1, 17, 1000, 128), (2, 100, 77, 6
              (4, 64, 4096, 256), (5, 65, 31, 32), (6, 40, 384, 96), (16, 96, 640, 64), (17, 130, 129, 32),
              (33, 50, 300, 1000), (64, 70, 512, 128), (65, 16, 96, 32), (130, 130, 130, 32), (200, 33, 64, 64),
              (48, 20, 1100, 64), (90, 36, 700, 128), (3, 20, 8200, 128), (16, 33, 9000, 32),
-             (250, 4090, 1100, 64), (130, 8200, 321, 32), (32, 16390, 200, 128), (256, 4100, 1536, 256)]
+             (250, 4090, 1100, 64), (130, 8200, 321, 32), (32, 16390, 200, 128), (256, 4100, 1536, 256), (150, 4090, 321, 32),
+             (60, 8190, 200, 64), (60, 4090, 130, 96)]
 
 
 @pytest.mark.parametrize("pad", [0, 16, 3])
