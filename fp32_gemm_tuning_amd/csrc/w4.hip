@@ -537,7 +537,11 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
             transpose4(d[b]);
         }
         const i32x4* st = xs + p % STAGES * (C::PARTS * UNITS);
-        f32x4 part[NB][MB], sx[MB];
+        // FP32: the sums of X's leading parts apart from those of the others. Leading
+        // parts have 8 bits and numbers 5, so their sums over a group lose almost nothing
+        // before the zero point is taken off; the others' are 2^-8 of them.
+        constexpr int KINDS = C::PARTS > 1 ? 2 : 1;
+        f32x4 part[KINDS][NB][MB], sx[KINDS][MB];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (k0 + 32 * j >= a.K) break;
@@ -548,16 +552,19 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
                 if (j % PER == 0) {
-                    sx[i] = none;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) part[b][i] = none;
+                    for (int kind = 0; kind < KINDS; ++kind) {
+                        sx[kind][i] = none;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) part[kind][b][i] = none;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < C::PARTS; ++e) {
                     const i32x4 x = st[e * UNITS + k8 * ROWS + ((16 * i + c) ^ (k8 & 15))];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) part[b][i] = C::mma(x, u[b], part[b][i]);
-                    sx[i] = C::mma(x, ones, sx[i]);
+                    for (int b = 0; b < NB; ++b) part[e > 0][b][i] = C::mma(x, u[b], part[e > 0][b][i]);
+                    sx[e > 0][i] = C::mma(x, ones, sx[e > 0][i]);
                 }
             }
             if ((j + 1) % PER == 0 || k0 + 32 * (j + 1) >= a.K) {
@@ -569,8 +576,11 @@ __global__ __launch_bounds__(NW * 64) void k_w4_rows(W4Args a, W4Groups gr) {
 #pragma unroll
                     for (int i = 0; i < MB; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[b][i][e] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[i][e], part[b][i][e]), acc[b][i][e]);
+                        for (int e = 0; e < 4; ++e) {
+                            float v = __builtin_fmaf(-z, sx[0][i][e], part[0][b][i][e]);
+                            if constexpr (KINDS == 2) v += __builtin_fmaf(-z, sx[1][i][e], part[1][b][i][e]);
+                            acc[b][i][e] = __builtin_fmaf(s, v, acc[b][i][e]);
+                        }
                 }
             }
         }

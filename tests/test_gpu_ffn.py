@@ -373,6 +373,23 @@ def test_w4_random(dev, shape, dtype, zeros):
         _close(sg.w4_glu(X, *w, act), a * u, e, act)
 
 
+@pytest.mark.parametrize("M", [9, 200])
+@pytest.mark.parametrize("zeros", [False, True], ids=["symmetric", "zeros"])
+def test_w4_keeps_single_precision(dev, zeros, M):
+    """One group, |x| in [1/2, 2): the sums of 8-bit leading parts are exact
+    (93 * 31 * 2 < 2^13, in steps of 2^-8), so three roundings of results remain
+    (the zero point's, the rest's and the scale's), at most 2^-24 each in the norm, and
+    those of the rest's sums, 2^-7 of the products: 4 * 2^-24 in all."""
+    gen = _gen(21, M, zeros)
+    _say("w4 fp32", M, zeros)
+    X = torch.rand(M, 93, generator=gen) * 1.5 + 0.5
+    X = (X * torch.where(torch.rand(M, 93, generator=gen) < 0.5, -1.0, 1.0)).to(dev)
+    w = sg.w4_quantize(torch.randn(97, 93, generator=gen).to(dev), 256, zeros)
+    want = X.double() @ ref.w4_values(*w).T
+    got = sg.w4_matmul(X, w).double()
+    assert float((got - want).norm() / want.norm()) <= 4 * 2.0 ** -24
+
+
 def test_w4_rows_stay_apart(dev):
     # NaN and infinities in one row of X, and a NaN scale in one row of W,
     # show in that row and column only.
