@@ -1,7 +1,6 @@
-// Tile kernels of the gated block: the forward pass (both projections, the
-// activation and the product in one kernel) and, for 16-bit types, the two
-// products of the backward pass. FP32's backward products go through the
-// library's own dispatch (ffn_api.hip).
+// Kernels of the gated block: the forward pass (both projections, the activation
+// and the product in one kernel) and the two products of the backward pass.
+// Large FP32 ones of those go through the library's own dispatch (ffn_api.hip).
 #include "glu_core.hpp"
 
 namespace sgemm {
@@ -91,6 +90,88 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_fwd(GluArgs a, int tiles_m, int 
             }
             h.flush((T*)a.H + f, a.ldh, row, a.M, a.F - f);
         }
+}
+
+// Sums over the wave's 64 lanes, of four values at a time: lane 16 r + x ends with
+// value r's, in an order of additions that is fixed.
+template <int CTRL>
+__device__ __forceinline__ float plus_dpp(float v) {
+    const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true);
+    return v + __builtin_bit_cast(float, o);
+}
+__device__ __forceinline__ float lane_sums(float a, float b, float c, float d) {
+    auto halves = [](float x, float y) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
+                                                        __builtin_bit_cast(uint32_t, y), false, false);
+        return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+    };
+    const float p = halves(a, c), q = halves(b, d);
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, p), __builtin_bit_cast(uint32_t, q),
+                                                    false, false);
+    float v = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+    v = plus_dpp<0xB1>(v);
+    v = plus_dpp<0x4E>(v);
+    v = plus_dpp<0x141>(v);
+    return plus_dpp<0x140>(v);
+}
+
+// The forward pass of very few rows on the vector units: a workgroup takes two
+// features (four weight rows) and up to MR rows of X, and its four waves take K's
+// kibibytes of each in turn, so that even a layer of a thousand features has all compute
+// units reading its weights; 16 to 32 waves a unit keep enough loads in flight
+// without a ring. Bound by the weights' bytes: one row of 8192 x 4096 bf16 23.9 us
+// (134 MB, 5.6 TB/s), FP32 46 (5.8 TB/s); a row more costs MR's multiply-adds, 8 of FP32 62.
+template <class T, int MR, bool SHORT>
+__global__ __launch_bounds__(256) void k_glu_few(GluArgs a) {
+    constexpr int EPC = Elem<T>::EPC, FW = 2, STEP = 64 * EPC;
+    typedef T Vec __attribute__((ext_vector_type(EPC)));
+    __shared__ float red[4][MR][4];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int f0 = blockIdx.x * FW, m0 = blockIdx.y * MR;
+    const Lines<T> lx = {(const T*)a.X, a.ldx, a.M, a.K};
+    const Lines<T> lw[2] = {{(const T*)a.Wg, a.ldwg, a.F, a.K}, {(const T*)a.Wu, a.ldwu, a.F, a.K}};
+    float acc[MR][4] = {};   // [row][2 matrix + feature]
+    for (int k0 = w * STEP; k0 < a.K; k0 += 4 * STEP) {
+        const int at = k0 + lane * EPC;
+        i32x4 v[4], x[MR];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = load_chunk<SHORT>(lw[i >> 1], f0 + (i & 1), at);
+#pragma unroll
+        for (int m = 0; m < MR; ++m) x[m] = load_chunk<SHORT>(lx, m0 + m, at);
+        if (k0 + STEP > a.K) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = place_chunk<SHORT>(v[i], lw[i >> 1], f0 + (i & 1), at);
+#pragma unroll
+            for (int m = 0; m < MR; ++m) x[m] = place_chunk<SHORT>(x[m], lx, m0 + m, at);
+        }
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            const Vec xs = __builtin_bit_cast(Vec, x[m]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const Vec vs = __builtin_bit_cast(Vec, v[i]);
+#pragma unroll
+                for (int e = 0; e < EPC; ++e) acc[m][i] = __builtin_fmaf((float)xs[e], (float)vs[e], acc[m][i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+        const float v = lane_sums(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+        if ((lane & 15) == 0) red[w][m][lane >> 4] = v;
+    }
+    __syncthreads();
+    const int m = threadIdx.x >> 1, f = threadIdx.x & 1;
+    if (m < MR && m0 + m < a.M && f0 + f < a.F) {
+        const float g = red[0][m][f] + red[1][m][f] + red[2][m][f] + red[3][m][f];
+        const float u = red[0][m][2 + f] + red[1][m][2 + f] + red[2][m][2 + f] + red[3][m][2 + f];
+        if (a.P != nullptr) {
+            float* p = a.P + (int64_t)(m0 + m) * a.ldp + f0 + f;
+            p[0] = g;
+            p[a.F] = u;
+        }
+        ((T*)a.H)[(int64_t)(m0 + m) * a.ldh + f0 + f] = (T)(act_value<sizeof(T) == 4>(a.act, g) * u);
+    }
 }
 
 // The forward pass of few rows: the weights' bytes are the work. A workgroup takes
@@ -428,11 +509,35 @@ static hipError_t launch_glu_rows(const GluArgs& a, bool dma, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <class T, int MR>
+static hipError_t launch_glu_few(const GluArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)cdiv(a.F, 2), (unsigned)cdiv(a.M, MR));
+    if (a.K < Elem<T>::EPC)
+        hipLaunchKernelGGL((k_glu_few<T, MR, true>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_glu_few<T, MR, false>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s) {
     const bool dma = dma_ok(dtype, a.X, a.ldx, a.K, 256) && dma_ok(dtype, a.Wg, a.ldwg, a.K, 128) &&
                      dma_ok(dtype, a.Wu, a.ldwu, a.K, 128);
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
+        // Very few rows, or few features: the vector units. In us, here against
+        // k_glu_rows: F x K = 8192 x 4096 bf16 one row 24 and 35, four 26 and 35, eight
+        // 34 and 36 (odd sizes 44 and 34), FP32 eight 62 and 67, sixteen 98 and 66; 1024 x
+        // 4096 bf16 sixteen rows 10 and 13, 32 rows 15 and 14, FP32 15 and 43, 23
+        // and 43; 1810 x 7435 FP32 one row 22 and 136, 32 rows 78 and 129.
+        constexpr bool F32 = sizeof(T) == 4;
+        const int64_t times = cdiv(a.M, 8);   // that the weights are read
+        if (a.M <= 32 && cdiv(a.F, 2) <= max_workgroups(256) &&
+            (a.M <= 4 || (a.M <= 8 && F32) || times * a.F <= (F32 ? 8192 : 4096))) {
+            if (a.M <= 1) return launch_glu_few<T, 1>(a, s);
+            if (a.M <= 2) return launch_glu_few<T, 2>(a, s);
+            if (a.M <= 4) return launch_glu_few<T, 4>(a, s);
+            return launch_glu_few<T, 8>(a, s);
+        }
         // Few rows, or few tiles: the workgroups that split K (128 x 4096 x 4096
         // bf16 21 us against 35 on 64 x 64 tiles, 512 x 2048 x 2048 level).
         const int64_t wgs64 = cdiv(a.M, 64) * cdiv(a.F, 32), wgs32 = cdiv(a.M, 32) * cdiv(a.F, 32);

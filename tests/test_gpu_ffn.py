@@ -48,7 +48,8 @@ def _out(rows, cols, dtype, dev, pad=0, offset=0):
 # than one tile of every kernel
 SHAPES = [(1, 1, 1), (1, 7, 1000), (2, 300, 8), (3, 65, 31), (5, 64, 64), (16, 96, 256), (17, 33, 65),
           (32, 130, 520), (33, 64, 72), (64, 128, 128), (70, 31, 513), (128, 64, 192), (129, 257, 191),
-          (300, 200, 77), (257, 512, 64)]
+          (300, 200, 77), (257, 512, 64), (2, 9, 2), (4, 17, 3), (6, 40, 3), (12, 3800, 90), (9, 8200, 40),
+          (2, 33, 2100)]
 # (pad, offset) of every operand's rows, in elements
 LAYOUTS = [(0, 0), (8, 8), (3, 1)]
 
