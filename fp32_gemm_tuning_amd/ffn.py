@@ -17,7 +17,8 @@ Tensor helpers (CUDA tensors of one type -- float32, bfloat16 or float16 -- on
 one device, 2-D with unit column stride; any row stride). They check their
 arguments, raise SgemmError for a C error code, enqueue on `stream` (default:
 the current stream of the tensors' device) and return their outputs; an output
-that is not given is allocated:
+that is not given is allocated. No autograd graph is recorded; glu_backward is
+called explicitly:
     glu(X, Wg, Wu, act="silu", out=None, preact=None, stream=None)
     glu_backward(dH, X, Wg, Wu, preact, act="silu", dX=None, dWg=None, dWu=None,
                  workspace=None, stream=None)
@@ -207,7 +208,7 @@ def glu(X, Wg, Wu, act: str = "silu", out=None, preact=None, stream=None):
     t = X.dtype
     ldp = 2 * F
     if preact is not None:
-            ldp = _ld(preact, X, torch.float32, M, 2 * F, "preact")
+        ldp = _ld(preact, X, torch.float32, M, 2 * F, "preact")
     _call(X, stream, "sgemm_f32_glu", d, _act(act), M, F, K, X.data_ptr(), _ld(X, X, t, M, K, "X"),
           Wg.data_ptr(), _ld(Wg, X, t, F, K, "Wg"), Wu.data_ptr(), _ld(Wu, X, t, F, K, "Wu"), H.data_ptr(),
           _ld(H, X, t, M, F, "out"), None if preact is None else preact.data_ptr(), max(ldp, 1))
@@ -255,7 +256,7 @@ def glu_backward_workspace(X, F: int) -> int:
     d = _gpu(X, "X")
     cus = _cus.get(X.get_device())
     if cus is None:
-            cus = _cus[X.get_device()] = torch.cuda.get_device_properties(X.device).multi_processor_count
+        cus = _cus[X.get_device()] = torch.cuda.get_device_properties(X.device).multi_processor_count
     rc, need = sgemm_f32_glu_bwd_ws_size(d, X.shape[0], F, X.shape[1], cus)
     if rc != 0:
         raise SgemmError(rc, "sgemm_f32_glu_bwd_ws_size")
@@ -304,7 +305,9 @@ def w4_dequantize(w: W4, out=None, stream=None):
 
 
 def w4_matmul(X, w: W4, out=None, stream=None):
-    """X W^T with W in 4 bits. X: (M, K); returns (M, F)."""
+    """X W^T with W in 4 bits. X: (M, K); returns (M, F). Made for batches of a
+    few hundred rows: 16-bit prompts longer than that are faster through
+    w4_dequantize and a product."""
     d = _gpu(X, "X")
     M = X.shape[0]
     F, q, s, z = _w4(w, X, "w")
