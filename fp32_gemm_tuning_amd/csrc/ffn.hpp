@@ -109,6 +109,10 @@ struct GluGradArgs {
     int64_t ldp, lddh, ldd;
     int32_t M, F;
     int32_t act;
+    // Half: the largest finite magnitude that each workgroup of k_glu_peak found
+    // (glu_peaks of them), and the power of two that dG and dU are kept times.
+    float* peaks;
+    int32_t* shift;
 };
 
 // A product of the backward pass. dX: C0 = dG W[0] + dU W[1]; dW:
@@ -124,6 +128,7 @@ struct GluProdArgs {
     float* part;
     int64_t ldd, ldw[2], ldx, ldc[2];
     int32_t M, F, K;
+    const int32_t* shift;   // half: D and L are kept times 2^*shift, or null
 };
 
 // A call over 4-bit weights: one matrix (w4) or two (w4_glu).
@@ -170,6 +175,7 @@ size_t glu_prod_bytes(int dtype, int64_t M, int64_t F, int64_t K);
 hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s);
 hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s);
 // glu_grad.hip
+int32_t glu_peaks(int64_t M, int64_t ldd);
 int check_glu_grad(const GluGradArgs& a);
 hipError_t launch_glu_grad(int dtype, const GluGradArgs& a, hipStream_t s);
 // w4.hip

@@ -42,10 +42,11 @@ int32_t group_of(int64_t group, int64_t K) {
 // The backward pass's workspace: dG and dU, each M rows of ldd elements (F
 // rounded up to whole 64-element slices, so that their rows are whole 16-byte
 // chunks), where they are kept in two parts their second ones, then the partial sums of products that are split, or, for large
-// FP32 products, what the stream-K kernels may use.
+// FP32 products, what the stream-K kernels may use, and for half the power of two
+// that dG and dU are kept times, with the magnitudes it comes from.
 struct BwdSpace {
     int64_t ldd;
-    size_t one, sk_at, sk_bytes, total;   // dG at 0, the others `one` apart
+    size_t one, sk_at, sk_bytes, shift_at, total;   // dG at 0, the others `one` apart
 };
 int bwd_space(int dtype, int64_t M, int64_t F, int64_t K, int num_cus, BwdSpace* o) {
     o->ldd = cdiv(F > 0 ? F : 1, 64) * 64;
@@ -65,7 +66,10 @@ int bwd_space(int dtype, int64_t M, int64_t F, int64_t K, int num_cus, BwdSpace*
         most = dw > most ? dw : most;
     }
     o->sk_bytes = up256(most);
-    o->total = o->sk_at + o->sk_bytes;
+    o->shift_at = o->sk_at + o->sk_bytes;
+    o->total = o->shift_at;
+    if (dtype == SGEMM_F32_DTYPE_F16 && M > 0 && F > 0)
+        o->total += up256(16 + sizeof(float) * (size_t)glu_peaks(M, o->ldd));
     return 0;
 }
 
@@ -206,9 +210,11 @@ SGEMM_F32_API int sgemm_f32_glu_bwd(int dtype, int act, int64_t M, int64_t F, in
 
     const bool two = glu_two_parts(dtype, M, F);
     char* const second[2] = {two ? ws + 2 * sp.one : nullptr, two ? ws + 3 * sp.one : nullptr};
+    int32_t* const shift = grads && dtype == SGEMM_F32_DTYPE_F16 ? (int32_t*)(ws + sp.shift_at) : nullptr;
     GluProdArgs p = {{ws, ws + sp.one}, {second[0], second[1]}, {Wg, Wu}, X, {nullptr, nullptr}, (float*)(ws + sp.sk_at), sp.ldd, {ldwg, ldwu}, ldx,
-                     {0, 0}, (int32_t)M, (int32_t)F, (int32_t)K};
-    const GluGradArgs g = {P, dH, ws, ws + sp.one, second[0], second[1], ldp, lddh, sp.ldd, (int32_t)M, (int32_t)F, act};
+                     {0, 0}, (int32_t)M, (int32_t)F, (int32_t)K, shift};
+    const GluGradArgs g = {P, dH, ws, ws + sp.one, second[0], second[1], ldp, lddh, sp.ldd, (int32_t)M, (int32_t)F, act,
+                           (float*)(ws + sp.shift_at + 16), shift};
     rc = check_glu_grad(g);
     if (rc == 0) rc = check_glu_prod(p);
     if (rc) return rc;

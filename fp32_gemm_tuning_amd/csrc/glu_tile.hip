@@ -318,6 +318,21 @@ __device__ __forceinline__ void put(const GluProdArgs& a, int u, int rows, int m
     else
         put_rows<T, Tl, Core>(own, (T*)(u ? a.C[1] : a.C[0]), u ? a.ldc[1] : a.ldc[0], m0, n0, rows, a.K, acc);
 }
+// The sums of operands kept times a power of two (GluProdArgs::shift), without it:
+// exact, but for sums below FP32's normal range.
+template <class T, class Core>
+__device__ __forceinline__ void unscale(const GluProdArgs& a, f32x16 (&acc)[Core::BI][Core::BJ]) {
+    if constexpr (std::is_same_v<T, f16>) {
+        if (a.shift == nullptr) return;
+        const int n = -*a.shift;
+#pragma unroll
+        for (int i = 0; i < Core::BI; ++i)
+#pragma unroll
+            for (int j = 0; j < Core::BJ; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_amdgcn_ldexpf(acc[i][j][r], n);
+    }
+}
 // This part's slices of n.
 __device__ __forceinline__ void part_of(int n, int& begin, int& end) {
     const int per = (n + gridDim.z - 1) / gridDim.z;
@@ -350,6 +365,7 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dx(GluProdArgs a, int tiles_m, i
         return (s - u * half) * Elem<T>::SLICE;
     };
     char* const own = product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
+    unscale<T, Core>(a, acc);
     put<T, Tl, Core>(a, 0, a.M, m0, n0, own, acc);
 }
 
@@ -375,6 +391,7 @@ __global__ __launch_bounds__(Tl::NT) void k_glu_dw(GluProdArgs a, int tiles_m, i
         return s * Elem<T>::SLICE;
     };
     char* const own = product<Core, Tl::DMA>(m0, n0, s0, s1, src, acc);
+    unscale<T, Core>(a, acc);
     put<T, Tl, Core>(a, u, a.F, m0, n0, own, acc);
 }
 

@@ -26,7 +26,11 @@
  * exact and sums are held in FP32 whatever the type; outputs are rounded
  * once. Where a 16-bit call has to keep a value between two products (dG and
  * dU, which the matrix cores read in the type), it is rounded once more, or,
- * where M * F <= 16384, kept in two parts. G and U are kept for the backward
+ * where M * F <= 16384, kept in two parts. In half, which spans less than the
+ * gradients do, they are kept times a power of two, one for all of a call's,
+ * that brings the largest finite one to the top of the type's range: each is
+ * then off by half a step, or by 2^-40 of that largest one where this is more,
+ * and none overflows. G and U are kept for the backward
  * pass in FP32 (`P`), so that no rounding comes before the derivative.
  *
  * Infinities and NaN stay in the rows and columns whose sums they enter. With
