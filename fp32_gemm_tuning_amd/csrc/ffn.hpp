@@ -32,11 +32,14 @@ static inline int64_t dtype_bytes(int dtype) { return dtype == SGEMM_F32_DTYPE_F
 // as (1 + tanh v) / 2 = 1 / (1 + exp(-2v))) go through exp(-|x|) <= 1, which
 // neither overflows nor loses the small side; a slope's second term, whose
 // factor has underflowed to 0, is dropped rather than multiplied by a large g.
-// 16-bit results take the exponential and the reciprocal of the hardware (each
-// within 2^-22 of its value down to exp(-87), under half a step of the
-// types by far): with the library's, the epilogue of a 256 x 256 tile took
-// a tenth of the product's time. FP32 results take the library's exponential
-// and one Newton step on the reciprocal.
+// 16-bit results take the exponential and the reciprocal of the hardware: with
+// the library's, the epilogue of a 256 x 256 tile took a tenth of the product's
+// time. The hardware's exponential gives 0 below 2^-126, where g exp(g) is still an
+// ordinary bfloat16 number (silu(-90) = -7.4e-38), so exp(-|x|) is the square of
+// exp(-|x| / 2). Its relative error is that of the rounded argument and of its
+// factor 1 / (2 ln 2), doubled by the square, |x| 2^-23 and less (2^-20 at 8, 2^-16.5 at
+// 87), and a few 2^-23: under half a step of the types. FP32 results take the
+// library's exponential and one Newton step on the reciprocal.
 template <bool F32>
 __device__ __forceinline__ float sigmoid(float x) {
     const float m = -fabsf(x);
@@ -47,7 +50,8 @@ __device__ __forceinline__ float sigmoid(float x) {
         r = __builtin_amdgcn_rcpf(d);
         r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
     } else {
-        p = __builtin_amdgcn_exp2f(1.44269504088896341f * m);
+        const float q = __builtin_amdgcn_exp2f(0.72134752044448170f * m);
+        p = q * q;
         r = __builtin_amdgcn_rcpf(1.0f + p);
     }
     return x < 0.0f ? p * r : r;   // NaN: p and r are NaN
