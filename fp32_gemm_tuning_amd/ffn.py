@@ -17,8 +17,10 @@ Tensor helpers (CUDA tensors of one type -- float32, bfloat16 or float16 -- on
 one device, 2-D with unit column stride; any row stride). They check their
 arguments, raise SgemmError for a C error code, enqueue on `stream` (default:
 the current stream of the tensors' device) and return their outputs; an output
-that is not given is allocated. No autograd graph is recorded; glu_backward is
-called explicitly:
+that is not given is allocated, in memory of that stream's own. A call on a stream
+that is not the current one waits for nothing there, nor does the current one
+wait for the call. No autograd graph is recorded; glu_backward is called
+explicitly:
     glu(X, Wg, Wu, act="silu", out=None, preact=None, stream=None)
     glu_backward(dH, X, Wg, Wu, preact, act="silu", dX=None, dWg=None, dWu=None,
                  workspace=None, stream=None)
@@ -184,18 +186,21 @@ def _call(like, stream, entry: str, *args) -> None:
         raise SgemmError(rc, entry)
 
 
-def _kept(t, stream):
-    """`t`, allocated on the current stream, for work on `stream`: its memory is
-    not handed on before that work is done."""
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=t.device)
-        t.record_stream(stream)
+def _new(like, rows: int, cols: int, stream=None, dtype=None, returned: bool = True):
+    """A matrix for a call that works on `stream`, in memory of that stream's own:
+    what the current stream has set free may still be read or written by work
+    that waits there, which `stream` does not wait for. The caller may use what is
+    `returned` on the current stream (once that has waited for the call): its
+    memory is not handed on before such use is over."""
+    if stream is None:
+        return like.new_empty((rows, cols), dtype=dtype)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        t = like.new_empty((rows, cols), dtype=dtype)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(like.device))
     return t
-
-
-def _new(like, rows: int, cols: int, stream=None):
-    return _kept(like.new_empty((rows, cols)), stream)
 
 
 def glu(X, Wg, Wu, act: str = "silu", out=None, preact=None, stream=None):
@@ -236,7 +241,7 @@ def glu_backward(dH, X, Wg, Wu, preact, act: str = "silu", dX=None, dWg=None, dW
             args += [g.data_ptr(), _ld(g, X, t, rows, K, name)]
     need = glu_backward_workspace(X, F)
     if workspace is None:
-        workspace = _kept(torch.empty(need, dtype=torch.uint8, device=X.device), stream)
+        workspace = _new(X, 1, need, stream, torch.uint8, returned=False)
     elif workspace.device != X.device:
         raise ValueError(f"workspace is on {workspace.device}, not on {X.device}")
     elif not workspace.is_contiguous():
@@ -286,7 +291,7 @@ def w4_quantize(W, group: int = 128, zeros: bool = False, stream=None) -> W4:
     d = _gpu(W, "W")
     F, K = W.shape
     G = _groups(K, group)
-    q = _kept(torch.empty((F, (K + 1) // 2), dtype=torch.uint8, device=W.device), stream)
+    q = _new(W, F, (K + 1) // 2, stream, torch.uint8)
     s = _new(W, F, G, stream)
     z = _new(W, F, G, stream) if zeros else None
     _call(W, stream, "sgemm_f32_w4_quantize", d, F, K, group, W.data_ptr(), _ld(W, W, W.dtype, F, K, "W"),
