@@ -186,6 +186,15 @@ def _call(like, stream, entry: str, *args) -> None:
         raise SgemmError(rc, entry)
 
 
+def _checked(stream, device):
+    """`stream`, a torch stream of the operands' device, an address or None. A
+    kernel on another device's stream would run there, on memory that device
+    need not reach."""
+    if stream is not None and not isinstance(stream, int) and getattr(stream, "device", device) != device:
+        raise ValueError(f"the stream is on {stream.device}, the operands are on {device}")
+    return stream
+
+
 def _new(like, rows: int, cols: int, stream=None, dtype=None, returned: bool = True):
     """A matrix for a call that works on `stream`, in memory of that stream's own:
     what the current stream has set free may still be read or written by work
@@ -207,6 +216,7 @@ def glu(X, Wg, Wu, act: str = "silu", out=None, preact=None, stream=None):
     """act(X Wg^T) * (X Wu^T). X: (M, K), Wg and Wu: (F, K); returns (M, F).
     `preact`, a float32 (M, 2F) tensor, receives what glu_backward needs."""
     d = _gpu(X, "X")
+    stream = _checked(stream, X.device)
     M, K = X.shape
     F = Wg.shape[0]
     H = _new(X, M, F, stream) if out is None else out
@@ -227,6 +237,7 @@ def glu_backward(dH, X, Wg, Wu, preact, act: str = "silu", dX=None, dWg=None, dW
     where it is None, and left out (None in the result) where it is False.
     `workspace`: a CUDA tensor of at least glu_backward_workspace() bytes."""
     d = _gpu(X, "X")
+    stream = _checked(stream, X.device)
     M, K = X.shape
     F = Wg.shape[0]
     t = X.dtype
@@ -289,6 +300,7 @@ def _w4(w: W4, like, name: str):
 def w4_quantize(W, group: int = 128, zeros: bool = False, stream=None) -> W4:
     """W (F, K) in 4 bits, with zero points where `zeros`."""
     d = _gpu(W, "W")
+    stream = _checked(stream, W.device)
     F, K = W.shape
     G = _groups(K, group)
     q = _new(W, F, (K + 1) // 2, stream, torch.uint8)
@@ -302,6 +314,7 @@ def w4_quantize(W, group: int = 128, zeros: bool = False, stream=None) -> W4:
 def w4_dequantize(w: W4, out=None, stream=None):
     """The matrix (F, K) that `w` stands for, in the type of its scales."""
     d = _gpu(w.scales, "scales")
+    stream = _checked(stream, w.scales.device)
     F, q, s, z = _w4(w, w.scales, "w")
     out = _new(w.scales, F, w.K, stream) if out is None else out
     _call(w.scales, stream, "sgemm_f32_w4_dequantize", d, F, w.K, w.group, *q, *s, *z, out.data_ptr(),
@@ -314,6 +327,7 @@ def w4_matmul(X, w: W4, out=None, stream=None):
     few hundred rows: 16-bit prompts longer than that are faster through
     w4_dequantize and a product."""
     d = _gpu(X, "X")
+    stream = _checked(stream, X.device)
     M = X.shape[0]
     F, q, s, z = _w4(w, X, "w")
     Y = _new(X, M, F, stream) if out is None else out
@@ -326,6 +340,7 @@ def w4_glu(X, wg: W4, wu: W4, act: str = "silu", out=None, stream=None):
     """act(X Wg^T) * (X Wu^T) with both weights in 4 bits, of the same K,
     group and row strides."""
     d = _gpu(X, "X")
+    stream = _checked(stream, X.device)
     M = X.shape[0]
     F, qg, sg, zg = _w4(wg, X, "wg")
     Fu, qu, su, zu = _w4(wu, X, "wu")

@@ -67,3 +67,34 @@ def test_nothing_is_allocated_another_way():
     source = inspect.getsource(ffn)
     assert not re.search(r"torch\.(empty|zeros|ones|full)\w*\(", source)
     assert source.count("new_empty(") == inspect.getsource(ffn._new).count("new_empty(")
+
+
+class GpuTensor:
+    """What the helpers look at before they look at a stream."""
+    is_cuda, dtype = True, torch.bfloat16
+
+    def __init__(self, *shape):
+        self.shape, self.device = shape, torch.device("cuda:0")
+
+    def dim(self):
+        return 2
+
+
+class Elsewhere:
+    device = torch.device("cuda:1")
+    cuda_stream = 4096
+
+
+W = ffn.W4(GpuTensor(8, 32), GpuTensor(8, 1), None, 64, 64)
+X = GpuTensor(4, 64)
+
+
+@pytest.mark.parametrize("call", [
+    lambda s: ffn.glu(X, GpuTensor(8, 64), GpuTensor(8, 64), stream=s),
+    lambda s: ffn.glu_backward(GpuTensor(4, 8), X, GpuTensor(8, 64), GpuTensor(8, 64), None, stream=s),
+    lambda s: ffn.w4_quantize(GpuTensor(8, 64), stream=s), lambda s: ffn.w4_dequantize(W, stream=s),
+    lambda s: ffn.w4_matmul(X, W, stream=s), lambda s: ffn.w4_glu(X, W, W, stream=s)],
+    ids=["glu", "glu_backward", "w4_quantize", "w4_dequantize", "w4_matmul", "w4_glu"])
+def test_another_devices_stream_is_refused(call):
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        call(Elsewhere())
