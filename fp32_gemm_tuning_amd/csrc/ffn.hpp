@@ -174,7 +174,7 @@ static inline bool glu_two_parts(int dtype, int64_t M, int64_t F) {
 // Whether the backward products of these sizes run on launch_glu_dx and
 // launch_glu_dw (16-bit ones do) or, FP32, on sgemm_f32_ws.
 bool glu_dx_here(int dtype, int64_t M, int64_t K);
-bool glu_dw_here(int dtype, int64_t F, int64_t K);
+bool glu_dw_here(int dtype, int64_t F, int64_t K, int64_t ldd, int64_t ldx);
 size_t glu_prod_bytes(int dtype, int64_t M, int64_t F, int64_t K);
 hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s);
 hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s);

@@ -240,7 +240,7 @@ SGEMM_F32_API int sgemm_f32_glu_bwd(int dtype, int act, int64_t M, int64_t F, in
         }
         if (rc) return rc;
     }
-    if ((want_g || want_u) && glu_dw_here(dtype, F, K)) {
+    if ((want_g || want_u) && glu_dw_here(dtype, F, K, sp.ldd, ldx)) {
         p.C[0] = want_g ? dWg : nullptr;
         p.C[1] = want_u ? dWu : nullptr;
         p.ldc[0] = lddwg;

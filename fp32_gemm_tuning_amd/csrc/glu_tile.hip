@@ -498,7 +498,13 @@ static bool here(int dtype, int64_t rows, int64_t cols, int64_t copies) {
     return dtype != SGEMM_F32_DTYPE_F32 || cdiv(rows, 64) * cdiv(cols, 64) * copies <= 640;
 }
 bool glu_dx_here(int dtype, int64_t M, int64_t K) { return here(dtype, M, K, 1); }
-bool glu_dw_here(int dtype, int64_t F, int64_t K) { return here(dtype, F, K, 2); }
+// (Of rows too far apart for the 32-bit offsets that the library's kernels take
+// a transposed product's slice by, dW is made here too: tiles filled through
+// registers, by 64-bit addresses. dX's plain product has a form for such rows.)
+bool glu_dw_here(int dtype, int64_t F, int64_t K, int64_t ldd, int64_t ldx) {
+    const int64_t ld = ldd > ldx ? ldd : ldx;
+    return here(dtype, F, K, 2) || ld * 64 * 4 >= (int64_t)kRange;
+}
 size_t glu_prod_bytes(int dtype, int64_t M, int64_t F, int64_t K) {
     if (M == 0 || F == 0 || K == 0) return 0;
     size_t most = 0;
