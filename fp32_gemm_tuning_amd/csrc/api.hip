@@ -556,13 +556,15 @@ SGEMM_F32_API const char* sgemm_f32_strerror(int code) {
         case -3: return "argument 3 (K) is negative";
         case -5: return "argument 5 (A; X or W) is NULL or not aligned to its element";
         case -6: return "argument 6 (lda; ldx, ldw) is smaller than the contiguous extent of A as stored "
-                        "(max(1, K) for row-major, untransposed A)";
+                        "(max(1, K) for row-major, untransposed A; max(1, K) for ldx and ldw)";
         case -7: return "argument 7 (B; Wg, Q) is NULL or not aligned to its element";
         case -8: return "argument 8 (ldb; ldwg, ldq) is smaller than the contiguous extent of B as stored "
-                        "(max(1, N) for row-major, untransposed B)";
+                        "(max(1, N) for row-major, untransposed B; max(1, K) for ldwg, "
+                        "max(1, (K + 1) / 2) for ldq)";
         case -10: return "argument 10 (C; H, Y, W) is NULL or not aligned to its element";
         case -11: return "argument 11 (ldc; ldh, ldy, ldw) is smaller than the contiguous extent of C "
-                         "(max(1, N) row-major, max(1, M) column-major)";
+                         "(max(1, N) row-major, max(1, M) column-major; max(1, F) for ldh and ldy, "
+                         "max(1, K) for ldw)";
         case -12: return "output pointer is NULL";
         case -13: return "layout is neither SGEMM_F32_ROW_MAJOR nor SGEMM_F32_COL_MAJOR";
         case -14: return "transa is neither SGEMM_F32_NO_TRANS nor SGEMM_F32_TRANS";

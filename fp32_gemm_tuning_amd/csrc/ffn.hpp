@@ -166,8 +166,10 @@ int check_glu_prod(const GluProdArgs& a);
 // values carry the sums, the roundings of single ones show in the gradients
 // instead of averaging out (one part: the error's norm is 1.41 times that of
 // rounding the gradients alone, give or take 2% at 16384 values, and 1.5 times and
-// more for a few hundred; two parts: 1.00 times). The doubled sums
-// are small there.
+// more for a few hundred; two parts: 1.00 times). The doubled sums are small
+// there. Beyond, the gradients keep the 1.41: two parts would make it 1.00 at every
+// size, for 1431 -> 2262 us of a 4096 x 8192 x 4096 bf16 step, 119 -> 204 of a backward
+// pass of 512 x 4096 x 4096 and 20 -> 25 of 77 x 1000 x 511.
 static inline bool glu_two_parts(int dtype, int64_t M, int64_t F) {
     return dtype != SGEMM_F32_DTYPE_F32 && M * F <= 16384;
 }

@@ -323,9 +323,10 @@ def w4_dequantize(w: W4, out=None, stream=None):
 
 
 def w4_matmul(X, w: W4, out=None, stream=None):
-    """X W^T with W in 4 bits. X: (M, K); returns (M, F). Made for batches of a
-    few hundred rows: 16-bit prompts longer than that are faster through
-    w4_dequantize and a product."""
+    """X W^T with W in 4 bits. X: (M, K); returns (M, F). Made for batches of up to
+    some 300 rows: longer 16-bit prompts are faster through w4_dequantize and a
+    16-bit product of the program's own (the package's dense product, gemm(),
+    takes FP32 only)."""
     d = _gpu(X, "X")
     stream = _checked(stream, X.device)
     M = X.shape[0]
@@ -338,7 +339,8 @@ def w4_matmul(X, w: W4, out=None, stream=None):
 
 def w4_glu(X, wg: W4, wu: W4, act: str = "silu", out=None, stream=None):
     """act(X Wg^T) * (X Wu^T) with both weights in 4 bits, of the same K,
-    group and row strides."""
+    group and row strides. Made for batches of up to some 300 rows: longer 16-bit
+    prompts are faster through w4_dequantize of both weights and glu()."""
     d = _gpu(X, "X")
     stream = _checked(stream, X.device)
     M = X.shape[0]

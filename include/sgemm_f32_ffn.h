@@ -34,9 +34,9 @@
  * pass in FP32 (`P`), so that no rounding comes before the derivative.
  *
  * Infinities and NaN stay in the rows and columns whose sums they enter. With
- * 4-bit weights an infinity in X, or a value beyond 2^120 in magnitude, may give
- * NaN where the exact sum is finite or infinite (the numbers are summed before their
- * zero point is taken off), and parts of FP32 values below 2^-126 count as
+ * 4-bit weights an infinity in X, or values of a row whose magnitudes sum to more
+ * than 2^122, may give NaN or an infinity where the exact sum is finite (the numbers
+ * are summed before their zero point is taken off), and parts of FP32 values below 2^-126 count as
  * zero.
  *
  * Layout. Every matrix is row-major with unit column stride and a leading
@@ -136,7 +136,9 @@ SGEMM_F32_API int sgemm_f32_w4_quantize(int dtype, int64_t F, int64_t K, int64_t
                                         const void *W, int64_t ldw, void *Q, int64_t ldq, void *S,
                                         int64_t lds, void *Z, int64_t ldz, void *stream);
 
-/* W[n][k] = (q - zero) * scale, rounded once. Z NULL: zero = 8. */
+/* W[n][k] = (q - zero) * scale, rounded once where q - zero is exact in FP32 (as
+ * with whole zero points, which sgemm_f32_w4_quantize makes), and otherwise
+ * once more. Z NULL: zero = 8. */
 SGEMM_F32_API int sgemm_f32_w4_dequantize(int dtype, int64_t F, int64_t K, int64_t group,
                                           const void *Q, int64_t ldq, const void *S, int64_t lds,
                                           const void *Z, int64_t ldz, void *W, int64_t ldw,

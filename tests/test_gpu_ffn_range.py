@@ -131,3 +131,75 @@ def test_no_gradient_is_zero(dev):
     Wg, Wu = (_normal((60, 40), gen, dev, 0.2) for _ in range(2))
     for g in _step(torch.zeros(50, 60, dtype=HALF, device=dev), X, Wg, Wu):
         assert (g == 0).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_workgroups_find_the_largest(dev, kind):
+    # More values than one pass of all workgroups that look for the largest takes;
+    # it is the last one.
+    M, F, K = 1500, 1500, 40
+    print("[gpu] half, many workgroups", kind, flush=True)
+    x, wg, wu, h = KINDS[kind]
+    gen = _gen(35)
+    X, dH = _normal((M, K), gen, dev, x), _normal((M, F), gen, dev, h / 8)
+    Wg, Wu = (_normal((F, K), gen, dev, w * K ** -0.5) for w in (wg, wu))
+    dH[-1, -1] = h * 4
+    for name, a, (b, bound) in zip(("dX", "dWg", "dWu"), _step(dH, X, Wg, Wu),
+                                   _bounds(*(v.double() for v in (dH, X, Wg, Wu)), "silu")):
+        fits = b.abs() < 65000
+        d = (a.double() - b).abs()
+        assert fits.any() and (d <= bound)[fits].all(), name
+
+
+def test_a_graph_follows_its_inputs(dev):
+    # One captured step, replayed on gradients of other sizes: each replay scales
+    # by what it finds.
+    print("[gpu] half graph", flush=True)
+    gen = _gen(36)
+    M, F, K = 150, 260, 72
+    X, base = _normal((M, K), gen, dev, 1.0), _normal((M, F), gen, dev, 1.0)
+    Wg, Wu = (_normal((F, K), gen, dev, K ** -0.5) for _ in range(2))
+    dH = base.clone()
+    P = torch.empty(M, 2 * F, device=dev)
+    outs = [torch.empty(r, K, dtype=HALF, device=dev) for r in (M, F, F)]
+    ws = torch.empty(sg.glu_backward_workspace(X, F), dtype=torch.uint8, device=dev)
+
+    def step():
+        sg.glu(X, Wg, Wu, preact=P)
+        sg.glu_backward(dH, X, Wg, Wu, P, dX=outs[0], dWg=outs[1], dWu=outs[2], workspace=ws)
+
+    s = torch.cuda.Stream(dev)
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step()
+    for scale in (1.0, 2.0 ** -14, 2.0 ** 9, 0.0, 2.0 ** -20, 1.0):
+        dH.copy_(base * scale)
+        want = _step(dH.clone(), X, Wg, Wu)
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), scale
+    del g
+
+
+def test_one_workspace_for_calls_of_other_sizes(dev):
+    print("[gpu] half, one workspace", flush=True)
+    gen = _gen(37)
+    jobs = []
+    for M, F, K, h in ((300, 500, 64, 1e-4), (20, 40, 96, 5000.0), (500, 300, 33, 1.0)):
+        X, dH = _normal((M, K), gen, dev, 0.1), _normal((M, F), gen, dev, h)
+        Wg, Wu = (_normal((F, K), gen, dev, K ** -0.5) for _ in range(2))
+        P = torch.empty(M, 2 * F, device=dev)
+        sg.glu(X, Wg, Wu, preact=P)
+        jobs.append((dH, X, Wg, Wu, P))
+    ws = torch.empty(max(sg.glu_backward_workspace(j[1], j[2].shape[0]) for j in jobs), dtype=torch.uint8, device=dev)
+    alone = [sg.glu_backward(*j) for j in jobs]
+    for _ in range(2):
+        got = [sg.glu_backward(*j, workspace=ws) for j in jobs]
+        assert all(torch.equal(a, b) for x, y in zip(got, alone) for a, b in zip(x, y))
