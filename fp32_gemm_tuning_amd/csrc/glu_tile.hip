@@ -419,7 +419,8 @@ using TileBig = Tile<256, 256, 128, 64, 1, true>;
 // whole 16-byte chunks, and a tile's span within 31-bit byte offsets.
 static bool dma_ok(int dtype, const void* p, int64_t ld, int64_t extent, int64_t tile_lines) {
     const int64_t e = dtype_bytes(dtype), chunk = 16 / e;
-    return aligned16(p) && ld % chunk == 0 && extent % chunk == 0 &&
+    // (ld by itself first: a single line's may be anything)
+    return aligned16(p) && ld % chunk == 0 && extent % chunk == 0 && ld < (int64_t)kRange &&
            ((tile_lines - 1) * ld + extent) * e < (int64_t)kRange;
 }
 
@@ -503,7 +504,7 @@ bool glu_dx_here(int dtype, int64_t M, int64_t K) { return here(dtype, M, K, 1);
 // registers, by 64-bit addresses. dX's plain product has a form for such rows.)
 bool glu_dw_here(int dtype, int64_t F, int64_t K, int64_t ldd, int64_t ldx) {
     const int64_t ld = ldd > ldx ? ldd : ldx;
-    return here(dtype, F, K, 2) || ld * 64 * 4 >= (int64_t)kRange;
+    return here(dtype, F, K, 2) || ld >= (int64_t)kRange / (64 * 4);
 }
 size_t glu_prod_bytes(int dtype, int64_t M, int64_t F, int64_t K) {
     if (M == 0 || F == 0 || K == 0) return 0;

@@ -33,7 +33,8 @@
  * and none overflows. G and U are kept for the backward
  * pass in FP32 (`P`), so that no rounding comes before the derivative.
  *
- * Infinities and NaN stay in the rows and columns whose sums they enter. With
+ * Infinities and NaN stay in the rows and columns whose sums they enter. Where dG
+ * and dU are kept in two parts, an infinity in X or a weight gives NaN there. With
  * 4-bit weights an infinity in X, or values of a row whose magnitudes sum to more
  * than 2^122, may give NaN or an infinity where the exact sum is finite (the numbers
  * are summed before their zero point is taken off), and parts of FP32 values below 2^-126 count as

@@ -54,3 +54,34 @@ def test_far_rows_of_the_weights(K):
     assert max(float(v.abs().max()) for v in want) < 2 ** 24
     for name, a, b in zip(("dX", "dWg", "dWu"), sg.glu_backward(dH, X, *far, P, "relu", dWg=outs[0], dWu=outs[1]), want):
         assert torch.equal(a.double(), b), name
+
+
+@pytest.mark.parametrize("ld", [1 << 60, 1 << 40, (1 << 60) + 7])
+@pytest.mark.parametrize("dtype,F", [(1, 20000), (2, 20000), (0, 20000), (0, 64), (1, 64)])
+def test_any_leading_dimension_of_a_single_row(dtype, F, ld):
+    # One row of X, so its leading dimension is of no consequence. An infinity in it
+    # shows if the row is read for others: those, times zero, would make it NaN.
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    dev = torch.device("cuda:0")
+    print("[gpu] one row", dtype, F, ld, flush=True)
+    t = (torch.float32, torch.bfloat16, torch.float16)[dtype]
+    K = 64
+    X = torch.arange(1, K + 1, device=dev).to(t)[None]
+    two_parts = dtype != 0 and F <= 16384          # (an infinity times a second part of zero is NaN)
+    if not two_parts:
+        X[0, 3] = float("inf")
+    P = torch.ones(1, 2 * F, device=dev)           # G = U = 1: dG = dU = dH
+    dH = torch.ones(1, F, dtype=t, device=dev)
+    dWg, dWu = (torch.full((F, K), float("nan"), dtype=t, device=dev) for _ in range(2))
+    need = sg.glu_backward_workspace(X, F)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = sg.sgemm_f32_glu_bwd(dtype, 3, 1, F, K, X, ld, 0, K, 0, K, P, ld, dH, ld, 0, K, dWg, K, dWu, K, ws, need)
+    torch.cuda.synchronize()
+    assert rc == 0 and torch.equal(dWg, X.expand(F, K)) and torch.equal(dWu, X.expand(F, K))
+    H = torch.full((1, F), float("nan"), dtype=t, device=dev)
+    W = torch.ones(F, K, dtype=t, device=dev)
+    assert sg.sgemm_f32_glu(dtype, 3, 1, F, K, X, ld, W, K, W, K, H, ld, None, 1) == 0
+    torch.cuda.synchronize()
+    g = X.double().sum()
+    assert torch.equal(H, (g * g).to(t).expand(1, F))
