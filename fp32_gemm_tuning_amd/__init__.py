@@ -455,3 +455,9 @@ def gemm(A, B, C, alpha: float = 1.0, beta: float = 0.0, variant=None, stream=No
 from .ffn import (ACTS, W4, glu, glu_backward, glu_backward_workspace, sgemm_f32_glu,  # noqa: E402,F401
                   sgemm_f32_glu_bwd, sgemm_f32_glu_bwd_ws_size, sgemm_f32_w4, sgemm_f32_w4_dequantize,
                   sgemm_f32_w4_glu, sgemm_f32_w4_quantize, w4_dequantize, w4_glu, w4_matmul, w4_quantize)
+
+# The norm before that block, and its products in 8 bits (i8.py).
+from .i8 import (I8, i8_dequantize, i8_glu, i8_matmul, i8_quantize, rms_norm, rms_norm_backward,  # noqa: E402,F401
+                 rms_norm_backward_workspace, rms_norm_i8, sgemm_f32_i8, sgemm_f32_i8_dequantize,
+                 sgemm_f32_i8_glu, sgemm_f32_i8_quantize, sgemm_f32_rms_norm, sgemm_f32_rms_norm_bwd,
+                 sgemm_f32_rms_norm_bwd_ws_size, sgemm_f32_rms_norm_i8)

@@ -28,7 +28,7 @@ ARCH = os.environ.get("SGEMM_F32_ARCH", "gfx950")
 
 SOURCES = ["api.hip", "ladder.hip", "valu_main.hip", "mfma_pipe.hip", "mfma_kgroup.hip",
            "mfma_small.hip", "peak.hip", "ffn_api.hip", "glu_tile.hip", "glu_grad.hip", "w4.hip",
-           "w4_pack.hip"]
+           "w4_pack.hip", "i8_api.hip", "i8.hip", "norm.hip", "norm_bwd.hip"]
 
 CXXFLAGS = [
     f"--offload-arch={ARCH}",

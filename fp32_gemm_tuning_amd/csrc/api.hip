@@ -557,14 +557,14 @@ SGEMM_F32_API const char* sgemm_f32_strerror(int code) {
         case -5: return "argument 5 (A; X or W) is NULL or not aligned to its element";
         case -6: return "argument 6 (lda; ldx, ldw) is smaller than the contiguous extent of A as stored "
                         "(max(1, K) for row-major, untransposed A; max(1, K) for ldx and ldw)";
-        case -7: return "argument 7 (B; Wg, Q) is NULL or not aligned to its element";
-        case -8: return "argument 8 (ldb; ldwg, ldq) is smaller than the contiguous extent of B as stored "
-                        "(max(1, N) for row-major, untransposed B; max(1, K) for ldwg, "
-                        "max(1, (K + 1) / 2) for ldq)";
-        case -10: return "argument 10 (C; H, Y, W) is NULL or not aligned to its element";
-        case -11: return "argument 11 (ldc; ldh, ldy, ldw) is smaller than the contiguous extent of C "
+        case -7: return "argument 7 (B; W, Wg, Q) is NULL or not aligned to its element";
+        case -8: return "argument 8 (ldb; ldw, ldwg, ldq) is smaller than the contiguous extent of B as stored "
+                        "(max(1, N) for row-major, untransposed B; max(1, K) for ldw, ldwg and the ldq of "
+                        "8-bit numbers, max(1, (K + 1) / 2) for that of 4-bit ones)";
+        case -10: return "argument 10 (C; H, Y, W, X) is NULL or not aligned to its element";
+        case -11: return "argument 11 (ldc; ldh, ldy, ldw, ldx) is smaller than the contiguous extent of C "
                          "(max(1, N) row-major, max(1, M) column-major; max(1, F) for ldh and ldy, "
-                         "max(1, K) for ldw)";
+                         "max(1, K) for ldw, and for the ldy and ldx of a norm and of 8-bit numbers)";
         case -12: return "output pointer is NULL";
         case -13: return "layout is neither SGEMM_F32_ROW_MAJOR nor SGEMM_F32_COL_MAJOR";
         case -14: return "transa is neither SGEMM_F32_NO_TRANS nor SGEMM_F32_TRANS";
@@ -577,22 +577,32 @@ SGEMM_F32_API const char* sgemm_f32_strerror(int code) {
         case -21: return "P is NULL or not 4-byte aligned";
         case -22: return "ldp is smaller than max(1, 2F)";
         case -23: return "dH is NULL or misaligned";
-        case -24: return "lddh is smaller than max(1, F)";
+        case -24: return "lddh is smaller than max(1, F) (a norm's: max(1, K))";
         case -25: return "dX is misaligned";
         case -26: return "lddx is smaller than max(1, K)";
-        case -27: return "dWg is misaligned";
+        case -27: return "dWg (dW) is misaligned";
         case -28: return "lddwg is smaller than max(1, K)";
         case -29: return "dWu is misaligned";
         case -30: return "lddwu is smaller than max(1, K)";
         case -31: return "group is neither a positive multiple of 32 nor at least K";
-        case -32: return "the scales (Sg) are NULL or misaligned";
+        case -32: return "the scales (S, Sw, Sg) are NULL or misaligned";
         case -33: return "lds is smaller than the number of groups";
         case -34: return "the zero points (Zg) are misaligned";
         case -35: return "ldz is smaller than the number of groups";
         case -36: return "Su is NULL or misaligned";
         case -37: return "Zu is misaligned, or only one of Zg and Zu is NULL";
+        case -38: return "R is misaligned";
+        case -39: return "ldr is smaller than max(1, K)";
+        case -40: return "eps is negative, infinite or NaN";
+        case -41: return "H is NULL where it is read, or misaligned";
+        case -42: return "ldh is smaller than max(1, K)";
+        case -43: return "rstd is NULL where it is read, or misaligned";
+        case -44: return "Sx is NULL or misaligned";
+        case -45: return "dY is NULL or misaligned";
+        case -46: return "lddy is smaller than max(1, K)";
         case SGEMM_F32_ERR_WORKSPACE: return "the workspace is smaller than the call needs "
-                                             "(sgemm_f32_ws_size, sgemm_f32_glu_bwd_ws_size)";
+                                             "(sgemm_f32_ws_size, sgemm_f32_glu_bwd_ws_size, "
+                                             "sgemm_f32_rms_norm_bwd_ws_size)";
         case SGEMM_F32_ERR_SCRATCH: return "the stream-K variant needs more workspace than the "
                                            "library's fixed scratch holds (SGEMM_F32_SCRATCH_BYTES)";
         case SGEMM_F32_ERR_VARIANT: return "variant id out of range";

@@ -1,12 +1,13 @@
 // The matrix-core tile of the gated block's products, for FP32, bfloat16 and
-// half operands with FP32 sums.
+// half operands with FP32 sums, and for int8 operands with int32 sums.
 //
 // All types share one tile geometry counted in 16-byte chunks: an operand's
-// part of a K slice is ROWS rows of 128 bytes (SLICE = 32 FP32 or 64 16-bit
-// k). The k index is only a summation index, so lane half h (lanes 32h ..
+// part of a K slice is ROWS rows of 128 bytes (SLICE = 32 FP32, 64 16-bit or 128
+// int8 k). The k index is only a summation index, so lane half h (lanes 32h ..
 // 32h + 31) walks its own half of the slice, chunk 4h + v at part v: one
 // 16-byte fragment feeds four v_mfma_f32_32x32x2_f32, or one
-// v_mfma_f32_32x32x16_{bf16,f16}, whose 8 k of a lane are 16 bytes.
+// v_mfma_f32_32x32x16_{bf16,f16}, whose 8 k of a lane are 16 bytes, or one
+// v_mfma_i32_32x32x32_i8, whose 16 are.
 //
 // An operand whose k runs along memory rows (KC) is stored [row][k] in LDS, chunk
 // q of row r at q ^ swz32(r) (common.hpp), so fragment reads and fills are free
@@ -28,13 +29,19 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
 // 16 bytes at an address aligned to its element only.
+typedef i32x4 i32x4_u1 __attribute__((aligned(1)));
 typedef i32x4 i32x4_u2 __attribute__((aligned(2)));
 
 template <class T>
 struct Elem {
     static constexpr int EPC = 16 / sizeof(T);   // elements per 16-byte chunk
     static constexpr int SLICE = 8 * EPC;        // k per slice (128 bytes)
+    using Unaligned = std::conditional_t<sizeof(T) == 1, i32x4_u1, i32x4_u2>;
+    using Sum = std::conditional_t<sizeof(T) == 1, int, float>;         // of products, and a block's sums
+    using Sums = std::conditional_t<sizeof(T) == 1, i32x16, f32x16>;
 };
 
 __device__ __forceinline__ void mma_chunk(float, const i32x4& a, const i32x4& b, f32x16& c) {
@@ -49,6 +56,10 @@ __device__ __forceinline__ void mma_chunk(bf16, const i32x4& a, const i32x4& b, 
 __device__ __forceinline__ void mma_chunk(f16, const i32x4& a, const i32x4& b, f32x16& c) {
     c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ void mma_chunk(int8_t, const i32x4& a, const i32x4& b, i32x16& c) {
+    c = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
 }
 
 // One lane's fragment of a transposed read: 8 k of one row, from two b64 reads.
@@ -83,7 +94,7 @@ template <bool SHORT, class T>
 __device__ __forceinline__ i32x4 load_chunk(const Lines<T>& s, int line, int at) {
     constexpr int EPC = Elem<T>::EPC;
     const T* p = s.p + (int64_t)(line < s.lines ? line : s.lines - 1) * s.ld;
-    if constexpr (!SHORT) return *(const i32x4_u2*)(p + (at < s.extent - EPC ? at : s.extent - EPC));
+    if constexpr (!SHORT) return *(const typename Elem<T>::Unaligned*)(p + (at < s.extent - EPC ? at : s.extent - EPC));
     typedef T Vec __attribute__((ext_vector_type(EPC)));
     Vec x = __builtin_bit_cast(Vec, i32x4{0, 0, 0, 0});
 #pragma unroll
@@ -224,7 +235,8 @@ struct WaveMap {
         wn = (mn % WAVES_N) * WN;
     }
     // `space`: 64 lanes x BI BJ 16 words for each wave, free to be written.
-    __device__ __forceinline__ void exchange(float* const* space, f32x16 (&acc)[BI][BJ]) const {
+    template <class T>
+    __device__ __forceinline__ void exchange(typename Elem<T>::Sum* const* space, typename Elem<T>::Sums (&acc)[BI][BJ]) const {
         if constexpr (KS > 1) {
 #pragma unroll
             for (int i = 0; i < BI; ++i)
@@ -240,7 +252,7 @@ struct WaveMap {
                 for (int j = 0; j < BJ; ++j)
 #pragma unroll
                     for (int r = 0; r < REGS; ++r) {
-                        float v = 0.0f;
+                        typename Elem<T>::Sum v = 0;
 #pragma unroll
                         for (int g = 0; g < KS; ++g)
                             v += space[mn + g * WAVES][((i * BJ + j) * 16 + kk * REGS + r) * 64 + lane];
@@ -256,12 +268,13 @@ struct TileCore {
     using Map = WaveMap<BM, BN, WM, WN, KS>;
     static constexpr int NT = Map::WAVES * KS * 64;
     static constexpr int BI = WM / 32, BJ = WN / 32;
+    using Sums = typename Elem<T>::Sums;
     static constexpr int STAGE = (BM + BN) * 128;
     static constexpr int PER_WAVE = 2 * STAGE / (Map::WAVES * KS);   // LDS of a wave's own, the product done
 
     template <class Src>
     __device__ __forceinline__ static void run(char* lds, int m0, int n0, int s_begin, int s_end, Src&& src,
-                                               f32x16 (&acc)[BI][BJ]) {
+                                               typename Elem<T>::Sums (&acc)[BI][BJ]) {
         const Map map;
         const int t = threadIdx.x, lane = map.lane, wm = map.wm, wn = map.wn;
 #pragma unroll
@@ -269,7 +282,7 @@ struct TileCore {
 #pragma unroll
             for (int j = 0; j < BJ; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
         if (s_begin >= s_end) return;
         struct Set {
             RegFill<T, BM, NT, ARC, SHORT> a;
@@ -328,10 +341,11 @@ struct TileCore {
             ring_barrier<63>();
         }
         if constexpr (KS > 1) {
-            float* const space[4] = {(float*)lds, (float*)(lds + STAGE / 2), (float*)(lds + STAGE),
-                                     (float*)(lds + STAGE + STAGE / 2)};
+            using Sum = typename Elem<T>::Sum;
+            Sum* const space[4] = {(Sum*)lds, (Sum*)(lds + STAGE / 2), (Sum*)(lds + STAGE),
+                                   (Sum*)(lds + STAGE + STAGE / 2)};
             static_assert(Map::WAVES * KS == 4 && BI * BJ * 16 * 64 * 4 <= STAGE / 2, "a wave's sums fit");
-            map.exchange(space, acc);
+            map.template exchange<T>(space, acc);
         }
     }
 };
@@ -421,6 +435,7 @@ struct DmaCore {
     using Map = WaveMap<BM, BN, WM, WN, KS>;
     static constexpr int NT = Map::WAVES * KS * 64;
     static constexpr int BI = WM / 32, BJ = WN / 32;
+    using Sums = typename Elem<T>::Sums;
     static constexpr int LDS_A = BM * 128, LDS_B = BN * 128;
     // LDS of a wave's own once the product is done.
     static constexpr int WAVES = Map::WAVES * KS, PER_WAVE = 2 * (LDS_A + LDS_B) / WAVES;
@@ -457,7 +472,7 @@ struct DmaCore {
     // src(s, A, B[2]) -> first k of slice s, with the operands' lines.
     template <class Src>
     __device__ __forceinline__ static void run(char* a0, char* b0, char* a1, char* b1, int m0, int n0,
-                                               int s_begin, int s_end, Src&& src, f32x16 (&acc)[BI][BJ]) {
+                                               int s_begin, int s_end, Src&& src, typename Elem<T>::Sums (&acc)[BI][BJ]) {
         const Map map;
         const int t = threadIdx.x, lane = map.lane, wm = map.wm, wn = map.wn;
 #pragma unroll
@@ -465,7 +480,7 @@ struct DmaCore {
 #pragma unroll
             for (int j = 0; j < BJ; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
         if (s_begin >= s_end) return;
         FA fa;
         FB fb;
@@ -523,10 +538,11 @@ struct DmaCore {
         if (s < s_end) slice(s, a0, b0, a1, b1);
         ring_barrier<0>();   // the loads past the last slice land before LDS is given up
         if constexpr (KS > 1) {
-            float* const space[4] = {(float*)a0, (float*)b0, (float*)a1, (float*)b1};
+            using Sum = typename Elem<T>::Sum;
+            Sum* const space[4] = {(Sum*)a0, (Sum*)b0, (Sum*)a1, (Sum*)b1};
             static_assert(Map::WAVES * KS == 4 && BI * BJ * 16 * 64 * 4 <= (LDS_A < LDS_B ? LDS_A : LDS_B),
                           "a wave's sums fit");
-            map.exchange(space, acc);
+            map.template exchange<T>(space, acc);
         }
     }
 };
@@ -594,4 +610,65 @@ struct RowsOut {
     }
 };
 
+constexpr int GLU_GROUP_M = 4;
+
+// A core's product in LDS of its own: two stages for each operand, as objects
+// apart so that the compiler can tell the stage being filled from the one
+// being read.
+// Returns LDS of the wave's own for the results.
+template <class Core, bool DMA, class Src>
+__device__ __forceinline__ char* product(int m0, int n0, int s_begin, int s_end, Src&& src,
+                                        typename Core::Sums (&acc)[Core::BI][Core::BJ]) {
+    if constexpr (DMA) {
+        __shared__ __attribute__((aligned(16))) char a0[Core::LDS_A], b0[Core::LDS_B], a1[Core::LDS_A],
+            b1[Core::LDS_B];
+        Core::run(a0, b0, a1, b1, m0, n0, s_begin, s_end, src, acc);
+        return Core::own(a0, b0, a1, b1);
+    } else {
+        __shared__ __attribute__((aligned(16))) char lds[2 * Core::STAGE];
+        Core::run(lds, m0, n0, s_begin, s_end, src, acc);
+        return lds + (threadIdx.x >> 6) * Core::PER_WAVE;
+    }
+}
+
+// Block and wave tile, and how it is filled: buffer-to-LDS loads (DMA) or
+// through registers, element by element where rows are shorter than 16 bytes.
+template <int BM_, int BN_, int WM_, int WN_, int KS_, bool DMA_, bool SHORT_ = false>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, NT = (BM_ / WM_) * (BN_ / WN_) * KS_ * 64;
+    static constexpr bool DMA = DMA_;
+    using Map = WaveMap<BM_, BN_, WM_, WN_, KS_>;
+    template <class T, bool ARC, bool BRC, bool PAIR>
+    using Core = std::conditional_t<DMA_, DmaCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, KS_>,
+                                    TileCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, KS_, SHORT_>>;
+};
+
+// Whether an operand of e-byte elements can be filled by buffer-to-LDS loads:
+// whole 16-byte chunks, and a tile's span within 31-bit byte offsets.
+static inline bool dma_ok(int64_t e, const void* p, int64_t ld, int64_t extent, int64_t tile_lines) {
+    const int64_t chunk = 16 / e;
+    // (ld by itself first: a single line's may be anything)
+    return aligned16(p) && ld % chunk == 0 && extent % chunk == 0 && ld < (int64_t)kRange &&
+           ((tile_lines - 1) * ld + extent) * e < (int64_t)kRange;
+}
+
+using TileReg = Tile<128, 128, 64, 64, 1, false>;
+using TileReg64 = Tile<64, 64, 32, 64, 2, false>;
+using TileDma64 = Tile<64, 64, 32, 64, 2, true>;
+using TileShort = Tile<128, 128, 64, 64, 1, false, true>;
+using TileMid = Tile<128, 128, 64, 64, 1, true>;
+using TileBig = Tile<256, 256, 128, 64, 1, true>;
+
+// Times that the choice of a tile goes by, in microseconds, measured on MI355X
+// (products of 300 x 1000 x 511 to 4096 x 8192 x 4096): a call takes about
+//     fixed + n max(alone, tiles per compute unit * busy)
+// for n slices, with `alone` a slice of a lone tile and `busy` a slice's share of a
+// unit that holds several.
+struct TileCost {
+    double fixed, alone, busy;
+    double of(int64_t tiles, int64_t slices) const {
+        const double per_unit = (double)((tiles + 255) / 256), b = per_unit * busy;
+        return fixed + (double)slices * (b > alone ? b : alone);
+    }
+};
 }  // namespace sgemm

@@ -5,39 +5,6 @@
 
 namespace sgemm {
 
-constexpr int GLU_GROUP_M = 4;
-
-// A core's product in LDS of its own: two stages for each operand, as objects
-// apart so that the compiler can tell the stage being filled from the one
-// being read.
-// Returns LDS of the wave's own for the results.
-template <class Core, bool DMA, class Src>
-__device__ __forceinline__ char* product(int m0, int n0, int s_begin, int s_end, Src&& src,
-                                        f32x16 (&acc)[Core::BI][Core::BJ]) {
-    if constexpr (DMA) {
-        __shared__ __attribute__((aligned(16))) char a0[Core::LDS_A], b0[Core::LDS_B], a1[Core::LDS_A],
-            b1[Core::LDS_B];
-        Core::run(a0, b0, a1, b1, m0, n0, s_begin, s_end, src, acc);
-        return Core::own(a0, b0, a1, b1);
-    } else {
-        __shared__ __attribute__((aligned(16))) char lds[2 * Core::STAGE];
-        Core::run(lds, m0, n0, s_begin, s_end, src, acc);
-        return lds + (threadIdx.x >> 6) * Core::PER_WAVE;
-    }
-}
-
-// Block and wave tile, and how it is filled: buffer-to-LDS loads (DMA) or
-// through registers, element by element where rows are shorter than 16 bytes.
-template <int BM_, int BN_, int WM_, int WN_, int KS_, bool DMA_, bool SHORT_ = false>
-struct Tile {
-    static constexpr int BM = BM_, BN = BN_, NT = (BM_ / WM_) * (BN_ / WN_) * KS_ * 64;
-    static constexpr bool DMA = DMA_;
-    using Map = WaveMap<BM_, BN_, WM_, WN_, KS_>;
-    template <class T, bool ARC, bool BRC, bool PAIR>
-    using Core = std::conditional_t<DMA_, DmaCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, KS_>,
-                                    TileCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, KS_, SHORT_>>;
-};
-
 // H = act(X Wg^T) * (X Wu^T). A tile's columns alternate between the two
 // weights in blocks of 32, so a wave holds G and U of the same outputs in
 // registers, and neither is written unless the backward pass wants them. Bound by the
@@ -408,35 +375,8 @@ __global__ __launch_bounds__(256) void k_glu_sum(GluProdArgs a, int rows, int pa
     ((T*)(u ? a.C[1] : a.C[0]))[row * (u ? a.ldc[1] : a.ldc[0]) + (at - row * a.K)] = (T)v;
 }
 
-using TileReg = Tile<128, 128, 64, 64, 1, false>;
-using TileReg64 = Tile<64, 64, 32, 64, 2, false>;
-using TileDma64 = Tile<64, 64, 32, 64, 2, true>;
-using TileShort = Tile<128, 128, 64, 64, 1, false, true>;
-using TileMid = Tile<128, 128, 64, 64, 1, true>;
-using TileBig = Tile<256, 256, 128, 64, 1, true>;
-
-// Whether an operand of `lines` lines can be filled by buffer-to-LDS loads:
-// whole 16-byte chunks, and a tile's span within 31-bit byte offsets.
-static bool dma_ok(int dtype, const void* p, int64_t ld, int64_t extent, int64_t tile_lines) {
-    const int64_t e = dtype_bytes(dtype), chunk = 16 / e;
-    // (ld by itself first: a single line's may be anything)
-    return aligned16(p) && ld % chunk == 0 && extent % chunk == 0 && ld < (int64_t)kRange &&
-           ((tile_lines - 1) * ld + extent) * e < (int64_t)kRange;
-}
-
-// Times that the choice of a tile goes by, in microseconds, measured on MI355X
-// (products of 300 x 1000 x 511 to 4096 x 8192 x 4096): a call takes about
-//     fixed + n max(alone, tiles per compute unit * busy)
-// for n slices, with `alone` a slice of a lone tile and `busy` a slice's share of a
-// unit that holds several. FP32 slices hold half the k and take the matrix
-// cores eight times as long; register-filled tiles wait longer per slice.
-struct TileCost {
-    double fixed, alone, busy;
-    double of(int64_t tiles, int64_t slices) const {
-        const double per_unit = (double)((tiles + 255) / 256), b = per_unit * busy;
-        return fixed + (double)slices * (b > alone ? b : alone);
-    }
-};
+// FP32 slices hold half the k and take the matrix cores eight times as long;
+// register-filled tiles wait longer per slice.
 // [FP32][filled through registers]
 static const TileCost kBig[2] = {{9.0, 1.8, 1.8}, {9.0, 7.3, 7.3}};
 static const TileCost kMid[2][2] = {{{7.0, 0.45, 0.52}, {7.0, 1.1, 0.85}}, {{7.0, 2.2, 2.0}, {7.0, 2.8, 2.2}}};
@@ -544,8 +484,8 @@ static hipError_t launch_glu_few(const GluArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_glu(int dtype, const GluArgs& a, hipStream_t s) {
-    const bool dma = dma_ok(dtype, a.X, a.ldx, a.K, 256) && dma_ok(dtype, a.Wg, a.ldwg, a.K, 128) &&
-                     dma_ok(dtype, a.Wu, a.ldwu, a.K, 128);
+    const bool dma = dma_ok(dtype_bytes(dtype), a.X, a.ldx, a.K, 256) && dma_ok(dtype_bytes(dtype), a.Wg, a.ldwg, a.K, 128) &&
+                     dma_ok(dtype_bytes(dtype), a.Wu, a.ldwu, a.K, 128);
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
         // Very few rows, or few features: the vector units. In us, here against
@@ -599,8 +539,8 @@ static hipError_t launch_sum(const GluProdArgs& a, int64_t rows, unsigned copies
 
 hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s) {
     // One tile's lines: 256 rows of dG, or a slice's 64 of W.
-    const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 256) && dma_ok(dtype, a.W[0], a.ldw[0], a.K, 64) &&
-                     dma_ok(dtype, a.W[1], a.ldw[1], a.K, 64) && a.ldw[0] == a.ldw[1];
+    const bool dma = dma_ok(dtype_bytes(dtype), a.D[0], a.ldd, a.ldd, 256) && dma_ok(dtype_bytes(dtype), a.W[0], a.ldw[0], a.K, 64) &&
+                     dma_ok(dtype_bytes(dtype), a.W[1], a.ldw[1], a.K, 64) && a.ldw[0] == a.ldw[1];
     const int n = dx_parts(dtype, a.M, a.F, a.K);
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
@@ -618,7 +558,7 @@ hipError_t launch_glu_dx(int dtype, const GluProdArgs& a, hipStream_t s) {
 
 hipError_t launch_glu_dw(int dtype, const GluProdArgs& a, hipStream_t s) {
     const unsigned both = a.C[0] != nullptr && a.C[1] != nullptr ? 2 : 1;
-    const bool dma = dma_ok(dtype, a.D[0], a.ldd, a.ldd, 64) && dma_ok(dtype, a.X, a.ldx, a.K, 64);
+    const bool dma = dma_ok(dtype_bytes(dtype), a.D[0], a.ldd, a.ldd, 64) && dma_ok(dtype_bytes(dtype), a.X, a.ldx, a.K, 64);
     const int n = dw_parts(dtype, a.M, a.F, a.K);
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;

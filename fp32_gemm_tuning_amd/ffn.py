@@ -195,18 +195,19 @@ def _checked(stream, device):
     return stream
 
 
-def _new(like, rows: int, cols: int, stream=None, dtype=None, returned: bool = True):
-    """A matrix for a call that works on `stream`, in memory of that stream's own:
+def _new(like, rows: int, cols: Optional[int], stream=None, dtype=None, returned: bool = True):
+    """A matrix (without `cols` a vector) for a call that works on `stream`, in memory of that stream's own:
     what the current stream has set free may still be read or written by work
     that waits there, which `stream` does not wait for. The caller may use what is
     `returned` on the current stream (once that has waited for the call): its
     memory is not handed on before such use is over."""
+    shape = (rows,) if cols is None else (rows, cols)
     if stream is None:
-        return like.new_empty((rows, cols), dtype=dtype)
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
-        t = like.new_empty((rows, cols), dtype=dtype)
+        t = like.new_empty(shape, dtype=dtype)
     if returned:
         t.record_stream(torch.cuda.current_stream(like.device))
     return t
