@@ -6,119 +6,283 @@ namespace sgemm {
 
 enum NormMode { NORM_Y, NORM_Q, PACK_Q };
 
-// Rows of any length: a workgroup a row, which is read again for every pass (from the sum H
-// where that was written: X may be the same memory).
+// One row of any length by the LANES lanes that hold it, N elements at a time, read again for every pass (from
+// the sum H where that was written: X may be the same memory): rows too long for registers, and,
+// element by element, which takes few registers, rows whose numbers are not ordinary.
+template <class T, NormMode MODE, int LANES, int N>
+__device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int lane, double* red) {
+    constexpr int STEP = LANES * N;
+    const int first = lane * N;
+    const T* x = (const T*)a.X + m * a.ldx;
+    const T* r = MODE != PACK_Q && a.R != nullptr ? (const T*)a.R + m * a.ldr : nullptr;
+    T* h = MODE != PACK_Q && a.H != nullptr ? (T*)a.H + m * a.ldh : nullptr;
+    const T* w = (const T*)a.W;
+    bool kept = false;   // H holds the sums
+    // The sum of the residual stream, rounded to the type, as FP32.
+    auto sum = [&](int at, Chunk<T, N>& c) {
+        if (kept) {
+            c.load(h, at, a.K);
+            return;
+        }
+        c.load(x, at, a.K);
+        if (r != nullptr) {
+            Chunk<T, N> d;
+            d.load(r, at, a.K);
+#pragma unroll
+            for (int e = 0; e < N; ++e) c.v[e] = (float)(T)(c.v[e] + d.v[e]);
+        }
+    };
+    float rstd = 1.0f;
+    if constexpr (MODE != PACK_Q) {
+        float ss = 0.0f;
+#pragma unroll 1
+        for (int at = first; at < a.K; at += STEP) {
+            Chunk<T, N> c;
+            sum(at, c);
+            if (h != nullptr) c.store(h, at, a.K);
+#pragma unroll
+            for (int e = 0; e < N; ++e) ss = __builtin_fmaf(c.v[e], c.v[e], ss);
+        }
+        kept = h != nullptr;
+        ss = over_row<LANES>(ss, Plus{}, (float*)red);
+        rstd = rstd_of(ss, a.K, a.eps);
+        if (sum_lost(ss, a.eps)) {
+            uint32_t top = 0;
+#pragma unroll 1
+            for (int at = first; at < a.K; at += STEP) {
+                Chunk<T, N> c;
+                sum(at, c);
+#pragma unroll
+                for (int e = 0; e < N; ++e) top = Max{}(top, __builtin_bit_cast(uint32_t, fabsf(c.v[e])));
+            }
+            top = over_row<LANES>(top, Max{}, (uint32_t*)red);
+            if (top > 0 && top < 0x7F800000u) {
+                const int shift = __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
+                ss = 0.0f;
+#pragma unroll 1
+                for (int at = first; at < a.K; at += STEP) {
+                    Chunk<T, N> c;
+                    sum(at, c);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float s = __builtin_amdgcn_ldexpf(c.v[e], -shift);
+                        ss = __builtin_fmaf(s, s, ss);
+                    }
+                }
+                ss = over_row<LANES>(ss, Plus{}, (float*)red);
+                rstd = rstd_scaled(ss, shift, a.K, a.eps);
+            }
+        }
+        if (a.rstd != nullptr && lane == 0) a.rstd[m] = rstd;
+    }
+    if constexpr (MODE == NORM_Y) {
+        T* y = (T*)a.Y + m * a.ldy;
+#pragma unroll 1
+        for (int at = first; at < a.K; at += STEP) {
+            Chunk<T, N> c, g;
+            sum(at, c);
+            g.load(w, at, a.K);
+#pragma unroll
+            for (int e = 0; e < N; ++e) c.v[e] = c.v[e] * rstd * g.v[e];
+            c.store(y, at, a.K);
+        }
+    } else {
+        // What is brought to 8 bits, in 64 bits: H W exactly, or X.
+        auto value = [&](int at, double (&v)[N]) {
+            Chunk<T, N> c, g;
+            sum(at, c);
+            if constexpr (MODE == NORM_Q) g.load(w, at, a.K);
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = MODE == NORM_Q ? (double)c.v[e] * (double)g.v[e] : (double)c.v[e];
+        };
+        double top = 0.0, bad = 0.0;
+#pragma unroll 1
+        for (int at = first; at < a.K; at += STEP) {
+            double v[N];
+            value(at, v);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                top = fmax(top, fabs(v[e]));
+                bad = __builtin_fma(v[e], 0.0, bad);   // 0, or NaN of an infinity or NaN
+            }
+        }
+        top = over_row<LANES>(top, Max{}, red);
+        bad = over_row<LANES>(bad, Plus{}, red);
+        const bool flat = !(bad == 0.0) || top == 0.0;
+        if (lane == 0)
+            a.S[m] = bad == 0.0 ? (a.K > 0 ? (float)(top * (double)rstd / 127.0) : 0.0f) : __builtin_nanf("");
+        const double inv = flat ? 0.0 : 127.0 / top;
+        int8_t* q = a.Q + m * a.ldq;
+#pragma unroll 1
+        for (int at = first; at < a.K; at += STEP) {
+            double v[N];
+            int n[N];
+            value(at, v);
+            levels(v, inv, flat ? 1.0 : top, n);
+#pragma unroll
+            for (int e = 0; e < N; ++e) n[e] = flat ? 0 : n[e];
+            store_levels(q, at, a.K, n);
+        }
+    }
+}
+
 constexpr int LONG_NT = 1024;
 template <class T, NormMode MODE>
 __global__ __launch_bounds__(LONG_NT) void k_norm_long(NormArgs a) {
-    constexpr int N = Chunk<T>::N, STEP = LONG_NT * N;
     __shared__ double red[LONG_NT / 64];
-    const int first = threadIdx.x * N;
-    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-        const T* x = (const T*)a.X + m * a.ldx;
-        const T* r = MODE != PACK_Q && a.R != nullptr ? (const T*)a.R + m * a.ldr : nullptr;
-        T* h = MODE != PACK_Q && a.H != nullptr ? (T*)a.H + m * a.ldh : nullptr;
-        const T* w = (const T*)a.W;
-        bool kept = false;   // H holds the sums
-        // The sum of the residual stream, rounded to the type, as FP32.
-        auto sum = [&](int at, Chunk<T>& c) {
-            if (kept) {
-                c.load(h, at, a.K);
-                return;
-            }
-            c.load(x, at, a.K);
-            if (r != nullptr) {
-                Chunk<T> d;
-                d.load(r, at, a.K);
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) norm_row<T, MODE, LONG_NT, Raw<T>::N>(a, m, threadIdx.x, red);
+}
+
+// Rows that stay in registers: LANES lanes hold a row in C chunks each, part of a wave, a wave or a
+// workgroup, so that it is read once. What leaves the ordinary
+// (squares or products next to the ends of FP32's range, infinities, NaN) is left to norm_row, which starts
+// anew: nothing has been written by then.
+template <class T, NormMode MODE, int LANES, int C, bool SHORT>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm(NormArgs a) {
+    constexpr int NT = LANES < 256 ? 256 : LANES, RPW = NT / LANES, N = Raw<T>::N;
+    __shared__ double red[NT / 64];
+    // A row's number is the same in all lanes of a wave or workgroup that holds it: its addresses are a
+    // scalar and an offset.
+    const int lane = RPW == 1 ? threadIdx.x : threadIdx.x % LANES;
+    const int sub = RPW == 1 ? 0 : LANES == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : threadIdx.x / LANES;
+    int at[C];
+    uint32_t place[C];
 #pragma unroll
-                for (int e = 0; e < N; ++e) c.v[e] = (float)(T)(c.v[e] + d.v[e]);
-            }
-        };
+    for (int c = 0; c < C; ++c) {
+        at[c] = (c * LANES + lane) * N;
+        place[c] = Raw<T>::template place_of<SHORT>(at[c], a.K);
+    }
+    // W stays in registers from row to row, or, where the longest rows leave no room, is read with each.
+    constexpr bool KEEP = MODE != PACK_Q && LANES * C < 4096;
+    Raw<T> w[C];
+    auto load_w = [&]() {
+#pragma unroll
+        for (int c = 0; c < C; ++c) w[c].template load<SHORT>((const T*)a.W, place[c], a.K);
+    };
+    if constexpr (KEEP) load_w();
+    for (int64_t m0 = (int64_t)blockIdx.x * RPW; m0 < a.M; m0 += (int64_t)gridDim.x * RPW) {
+        // Groups past the last row do its work again and write nothing.
+        const int64_t mine = m0 + sub, m = mine < a.M ? mine : a.M - 1;
+        const bool there = RPW == 1 || mine < a.M;
+        Raw<T> h[C], r[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            h[c].template load<SHORT>((const T*)a.X + m * a.ldx, place[c], a.K);
+        const bool add = MODE != PACK_Q && a.R != nullptr;
+        if (add) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                r[c].template load<SHORT>((const T*)a.R + m * a.ldr, place[c], a.K);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < N; ++e) h[c].v[e] = (T)((float)h[c].v[e] + (float)r[c].v[e]);
+        }
         float rstd = 1.0f;
+        bool usual = true;
         if constexpr (MODE != PACK_Q) {
             float ss = 0.0f;
-            for (int at = first; at < a.K; at += STEP) {
-                Chunk<T> c;
-                sum(at, c);
-                if (h != nullptr) c.store(h, at, a.K);
 #pragma unroll
-                for (int e = 0; e < N; ++e) ss = __builtin_fmaf(c.v[e], c.v[e], ss);
-            }
-            kept = h != nullptr;
-            ss = over_row<LONG_NT>(ss, Plus{}, (float*)red);
-            rstd = rstd_of(ss, a.K, a.eps);
-            if (sum_lost(ss)) {
-                uint32_t top = 0;
-                for (int at = first; at < a.K; at += STEP) {
-                    Chunk<T> c;
-                    sum(at, c);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) top = Max{}(top, __builtin_bit_cast(uint32_t, fabsf(c.v[e])));
-                }
-                top = over_row<LONG_NT>(top, Max{}, (uint32_t*)red);
-                if (top > 0 && top < 0x7F800000u) {
-                    const int shift = __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
-                    ss = 0.0f;
-                    for (int at = first; at < a.K; at += STEP) {
-                        Chunk<T> c;
-                        sum(at, c);
-#pragma unroll
-                        for (int e = 0; e < N; ++e) {
-                            const float s = __builtin_amdgcn_ldexpf(c.v[e], -shift);
-                            ss = __builtin_fmaf(s, s, ss);
-                        }
-                    }
-                    ss = over_row<LONG_NT>(ss, Plus{}, (float*)red);
-                    rstd = rstd_scaled(ss, shift, a.K, a.eps);
-                }
-            }
-            if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[m] = rstd;
-        }
-        if constexpr (MODE == NORM_Y) {
-            T* y = (T*)a.Y + m * a.ldy;
-            for (int at = first; at < a.K; at += STEP) {
-                Chunk<T> c, g;
-                sum(at, c);
-                g.load(w, at, a.K);
-#pragma unroll
-                for (int e = 0; e < N; ++e) c.v[e] = c.v[e] * rstd * g.v[e];
-                c.store(y, at, a.K);
-            }
-        } else {
-            // What is brought to 8 bits, in 64 bits: H W exactly, or X.
-            auto value = [&](int at, double (&v)[N]) {
-                Chunk<T> c, g;
-                sum(at, c);
-                if constexpr (MODE == NORM_Q) g.load(w, at, a.K);
-#pragma unroll
-                for (int e = 0; e < N; ++e) v[e] = MODE == NORM_Q ? (double)c.v[e] * (double)g.v[e] : (double)c.v[e];
-            };
-            double top = 0.0, bad = 0.0;
-            for (int at = first; at < a.K; at += STEP) {
-                double v[N];
-                value(at, v);
+            for (int c = 0; c < C; ++c) {
+                const bool whole = (c + 1) * LANES * N <= a.K;
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    top = fmax(top, fabs(v[e]));
-                    bad = __builtin_fma(v[e], 0.0, bad);   // 0, or NaN of an infinity or NaN
+                    float x = (float)h[c].v[e];
+                    if (!whole) x = Raw<T>::mine(at[c], place[c], e) ? x : 0.0f;
+                    ss = __builtin_fmaf(x, x, ss);
                 }
             }
-            top = over_row<LONG_NT>(top, Max{}, red);
-            bad = over_row<LONG_NT>(bad, Plus{}, red);
-            const bool flat = !(bad == 0.0) || top == 0.0;
-            if (threadIdx.x == 0)
-                a.S[m] = bad == 0.0 ? (a.K > 0 ? (float)(top * (double)rstd / 127.0) : 0.0f) : __builtin_nanf("");
-            const double inv = flat ? 0.0 : 127.0 / top;
-            int8_t* q = a.Q + m * a.ldq;
-            for (int at = first; at < a.K; at += STEP) {
-                double v[N];
-                int n[N];
-                value(at, v);
+            if constexpr (!KEEP) load_w();
+            ss = over_row<LANES>(ss, Plus{}, (float*)red);
+            rstd = rstd_of(ss, a.K, a.eps);
+            usual = !sum_lost(ss, a.eps);
+        }
+        auto keep = [&]() {
+            if constexpr (MODE != PACK_Q) {
+                if (a.H != nullptr) {
 #pragma unroll
-                for (int e = 0; e < N; ++e) n[e] = flat ? 0 : level(v[e], inv, top);
-                store_levels(q, at, a.K, n);
+                    for (int c = 0; c < C; ++c)
+                        if (at[c] < a.K) h[c].template store<SHORT>((T*)a.H + m * a.ldh, place[c], a.K);
+                }
+                if (a.rstd != nullptr && lane == 0) a.rstd[m] = rstd;
+            }
+        };
+        if constexpr (MODE == NORM_Y) {
+            if (usual && there) {
+                keep();
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    Raw<T> y;
+                    h[c].forget();
+                    w[c].forget();
+#pragma unroll
+                    for (int e = 0; e < N; ++e) y.v[e] = (T)((float)h[c].v[e] * rstd * (float)w[c].v[e]);
+                    if (at[c] < a.K) y.template store<SHORT>((T*)a.Y + m * a.ldy, place[c], a.K);
+                }
+            }
+        } else {
+            // 16-bit numbers and their products are FP32 numbers, FP32's products 64-bit ones.
+            using V = std::conditional_t<sizeof(T) == 4 && MODE == NORM_Q, double, float>;
+            auto value = [&](int c, int e) {
+                return MODE == NORM_Q ? (V)(float)h[c].v[e] * (V)(float)w[c].v[e] : (V)(float)h[c].v[e];
+            };
+            V top, inv;
+            if constexpr (sizeof(V) == 8) {
+                double t = 0.0, bad = 0.0;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    h[c].forget();
+                    w[c].forget();
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        t = fmax(t, fabs(value(c, e)));
+                        bad = __builtin_fma(value(c, e), 0.0, bad);
+                    }
+                }
+                t = over_row<LANES>(bad == 0.0 ? t : __builtin_inf(), Max{}, red);
+                usual = usual && t <= 1.0e300;
+                top = t;
+            } else {
+                // (as whole numbers, so that infinities and NaN are the largest)
+                uint32_t t = 0;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    h[c].forget();
+                    if constexpr (MODE != PACK_Q) w[c].forget();
+#pragma unroll
+                    for (int e = 0; e < N; ++e) t = Max{}(t, __builtin_bit_cast(uint32_t, fabsf((float)value(c, e))));
+                }
+                top = __builtin_bit_cast(float, over_row<LANES>(t, Max{}, (uint32_t*)red));
+                usual = usual && (ordinary(top) || top == 0.0f);
+                if (top == 0.0f) {   // zeros, or products that have become zero
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) any |= h[c].any();
+                    usual = usual && over_row<LANES>(any, Or{}, (uint32_t*)red) == 0;
+                }
+            }
+            inv = top > 0 ? (V)127 / top : 0;
+            if (usual && there) {
+                keep();
+                // (a row of zeros with eps = 0: 0 * infinity)
+                if (lane == 0) a.S[m] = (float)((double)top * (double)rstd / 127.0);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    V v[N];
+                    int q[N];
+                    h[c].forget();
+                    if constexpr (MODE != PACK_Q) w[c].forget();
+#pragma unroll
+                    for (int e = 0; e < N; ++e) v[e] = value(c, e);
+                    levels(v, inv, top, q);
+                    if constexpr (SHORT)
+                        store_levels(a.Q + m * a.ldq, at[c], a.K, q);
+                    else if (at[c] < a.K)
+                        Bytes<N>::store(a.Q + m * a.ldq + place[c], q);
+                }
             }
         }
+        if (!usual && there) norm_row<T, MODE, LANES, 1>(a, m, lane, red);
     }
 }
 
@@ -155,11 +319,31 @@ int check_i8_dequantize(const DequantArgs& a) {
     return dequantize_wgs(a) <= max_workgroups(256) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
+template <class T, NormMode MODE, int LANES, int C, bool SHORT = false>
+static hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
+    constexpr int NT = LANES < 256 ? 256 : LANES, RPW = NT / LANES;
+    // Eight waves a SIMD at most, whatever the rows: each workgroup keeps W for several.
+    const int64_t wgs = (a.M + RPW - 1) / RPW, most = 256 * 2048 / NT;
+    hipLaunchKernelGGL((k_norm<T, MODE, LANES, C, SHORT>), dim3((unsigned)(wgs < most ? wgs : most)), dim3(NT), 0, s, a);
+    return hipGetLastError();
+}
 template <NormMode MODE>
 static hipError_t launch(int dtype, const NormArgs& a, hipStream_t s) {
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        hipLaunchKernelGGL((k_norm_long<T, MODE>), dim3((unsigned)(a.M < (1 << 20) ? a.M : 1 << 20)), dim3(LONG_NT), 0, s, a);
+        constexpr int N = Raw<T>::N;
+        const int chunks = (a.K + N - 1) / N;
+        if (a.K > 0 && a.K < N) return launch_rows<T, MODE, 16, 1, true>(a, s);
+        if (a.K > 0 && chunks <= 16) return launch_rows<T, MODE, 16, 1>(a, s);
+        if (a.K > 0 && chunks <= 64) return launch_rows<T, MODE, 64, 1>(a, s);
+        if (a.K > 0 && chunks <= 128) return launch_rows<T, MODE, 64, 2>(a, s);
+        if (a.K > 0 && chunks <= 256) return launch_rows<T, MODE, 64, 4>(a, s);
+        if (a.K > 0 && chunks <= 512) return launch_rows<T, MODE, 256, 2>(a, s);
+        if (a.K > 0 && chunks <= 1024) return launch_rows<T, MODE, 256, 4>(a, s);
+        if (a.K > 0 && chunks <= 2048) return launch_rows<T, MODE, 1024, 2>(a, s);
+        if (a.K > 0 && chunks <= 4096) return launch_rows<T, MODE, 1024, 4>(a, s);
+        hipLaunchKernelGGL((k_norm_long<T, MODE>), dim3((unsigned)(a.M < (1 << 20) ? a.M : 1 << 20)), dim3(LONG_NT),
+                           0, s, a);
         return hipGetLastError();
     });
 }
