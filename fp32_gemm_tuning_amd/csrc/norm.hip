@@ -29,7 +29,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int lane,
             Chunk<T, N> d;
             d.load(r, at, a.K);
 #pragma unroll
-            for (int e = 0; e < N; ++e) c.v[e] = (float)(T)(c.v[e] + d.v[e]);
+            for (int e = 0; e < N; ++e) c.v[e] = (float)(T)as_f32(c.v[e] + d.v[e]);
         }
     };
     float rstd = 1.0f;
@@ -83,7 +83,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int lane,
             sum(at, c);
             g.load(w, at, a.K);
 #pragma unroll
-            for (int e = 0; e < N; ++e) c.v[e] = c.v[e] * rstd * g.v[e];
+            for (int e = 0; e < N; ++e) c.v[e] = as_f32(c.v[e] * rstd * g.v[e]);
             c.store(y, at, a.K);
         }
     } else {
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm(NormArgs 
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int e = 0; e < N; ++e) h[c].v[e] = (T)((float)h[c].v[e] + (float)r[c].v[e]);
+                for (int e = 0; e < N; ++e) h[c].v[e] = (T)as_f32((float)h[c].v[e] + (float)r[c].v[e]);
         }
         float rstd = 1.0f;
         bool usual = true;
@@ -184,12 +184,16 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm(NormArgs 
             float ss = 0.0f;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const bool whole = (c + 1) * LANES * N <= a.K;
+                if ((c + 1) * LANES * N <= a.K) {
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    float x = (float)h[c].v[e];
-                    if (!whole) x = Raw<T>::mine(at[c], place[c], e) ? x : 0.0f;
-                    ss = __builtin_fmaf(x, x, ss);
+                    for (int e = 0; e < N; ++e) ss = __builtin_fmaf((float)h[c].v[e], (float)h[c].v[e], ss);
+                } else {
+                    const int first = Raw<T>::first(at[c], place[c]);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float x = e >= first ? (float)h[c].v[e] : 0.0f;
+                        ss = __builtin_fmaf(x, x, ss);
+                    }
                 }
             }
             if constexpr (!KEEP) load_w();
@@ -216,7 +220,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm(NormArgs 
                     h[c].forget();
                     w[c].forget();
 #pragma unroll
-                    for (int e = 0; e < N; ++e) y.v[e] = (T)((float)h[c].v[e] * rstd * (float)w[c].v[e]);
+                    for (int e = 0; e < N; ++e) y.v[e] = (T)as_f32((float)h[c].v[e] * rstd * (float)w[c].v[e]);
                     if (at[c] < a.K) y.template store<SHORT>((T*)a.Y + m * a.ldy, place[c], a.K);
                 }
             }
@@ -286,37 +290,59 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm(NormArgs 
     }
 }
 
-// Values of matrices in 8 bits: 16 a thread.
+// Values of matrices in 8 bits: the chunks of 16 bytes of all rows in a line, four a thread, a workgroup's threads side
+// by side in each. Bound by the bytes written.
+constexpr int DQ_NT = 256, DQ_CHUNKS = 4;
 template <class T>
-__global__ __launch_bounds__(256) void k_i8_dequantize(DequantArgs a) {
-    const int chunks = (a.K + 15) / 16;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / chunks;
-    if (m >= a.M) return;
-    const int at = (int)(i - m * chunks) * 16;
-    const int8_t* q = a.Q + m * a.ldq + at;
-    const float s = a.S[m];
-    T* x = (T*)a.X + m * a.ldx;
-    constexpr int N = Chunk<T>::N;
-    int8_t v[16];
-    if (at + 16 <= a.K) {
-        __builtin_memcpy(v, q, 16);
-    } else {
+__global__ __launch_bounds__(DQ_NT) void k_i8_dequantize(DequantArgs a, int per_row) {
+    constexpr int N = Raw<T>::N;
+    typedef int W __attribute__((ext_vector_type(N / 4)));
+    typedef W Wu __attribute__((aligned(1)));
+    const int64_t chunk0 = (int64_t)blockIdx.x * (DQ_NT * DQ_CHUNKS), m0 = chunk0 / per_row;
+    const uint32_t rest = (uint32_t)(chunk0 - m0 * per_row) + threadIdx.x;
+    W v[DQ_CHUNKS];
+    int64_t m[DQ_CHUNKS];
+    uint32_t place[DQ_CHUNKS];   // the row's last elements where a chunk would reach past them
+    float s[DQ_CHUNKS];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = at + e < a.K ? q[e] : 0;
+    for (int c = 0; c < DQ_CHUNKS; ++c) {
+        const uint32_t i = rest + c * DQ_NT, r = i / (uint32_t)per_row;
+        m[c] = m0 + r < a.M ? m0 + r : a.M;
+        const int64_t row = m[c] < a.M ? m[c] : a.M - 1;
+        s[c] = a.S[row];
+        const int8_t* q = a.Q + row * a.ldq;
+        if (a.K >= N) {
+            place[c] = Raw<T>::template place_of<false>((int)(i - r * (uint32_t)per_row) * N, a.K);
+            v[c] = *(const Wu*)(q + place[c]);
+        } else {
+            place[c] = 0;
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j) v[c][j] = 0;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (e < a.K) v[c][e / 4] |= (q[e] & 255) << (8 * (e % 4));
+        }
     }
 #pragma unroll
-    for (int i0 = 0; i0 < 16; i0 += N) {
-        Chunk<T> c;
+    for (int c = 0; c < DQ_CHUNKS; ++c) {
+        Raw<T> y;
 #pragma unroll
-        for (int e = 0; e < N; ++e) c.v[e] = (float)v[i0 + e] * s;
-        c.store(x, at + i0, a.K);
+        for (int e = 0; e < N; ++e) y.v[e] = (T)as_f32((float)(int8_t)(v[c][e / 4] >> (8 * (e % 4))) * s[c]);
+        if (m[c] >= a.M) continue;
+        T* x = (T*)a.X + m[c] * a.ldx;
+        if (a.K >= N)
+            y.template store<false>(x, place[c], a.K);
+        else
+            y.template store<true>(x, 0, a.K);
     }
 }
 
-static int64_t dequantize_wgs(const DequantArgs& a) { return ((int64_t)a.M * ((a.K + 15) / 16) + 255) / 256; }
+static int64_t dequantize_wgs(const DequantArgs& a, int64_t per_row) {
+    return (a.M * per_row + DQ_NT * DQ_CHUNKS - 1) / (DQ_NT * DQ_CHUNKS);
+}
 
 int check_i8_dequantize(const DequantArgs& a) {
-    return dequantize_wgs(a) <= max_workgroups(256) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
+    return dequantize_wgs(a, (a.K + 3) / 4) <= max_workgroups(DQ_NT) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
 template <class T, NormMode MODE, int LANES, int C, bool SHORT = false>
@@ -333,14 +359,16 @@ static hipError_t launch(int dtype, const NormArgs& a, hipStream_t s) {
         using T = typename decltype(tag)::type;
         constexpr int N = Raw<T>::N;
         const int chunks = (a.K + N - 1) / N;
+        const bool few = a.M <= 256;
         if (a.K > 0 && a.K < N) return launch_rows<T, MODE, 16, 1, true>(a, s);
         if (a.K > 0 && chunks <= 16) return launch_rows<T, MODE, 16, 1>(a, s);
+        if (a.K > 0 && chunks <= 32) return launch_rows<T, MODE, 16, 2>(a, s);
         if (a.K > 0 && chunks <= 64) return launch_rows<T, MODE, 64, 1>(a, s);
         if (a.K > 0 && chunks <= 128) return launch_rows<T, MODE, 64, 2>(a, s);
         if (a.K > 0 && chunks <= 256) return launch_rows<T, MODE, 64, 4>(a, s);
         if (a.K > 0 && chunks <= 512) return launch_rows<T, MODE, 256, 2>(a, s);
-        if (a.K > 0 && chunks <= 1024) return launch_rows<T, MODE, 256, 4>(a, s);
-        if (a.K > 0 && chunks <= 2048) return launch_rows<T, MODE, 1024, 2>(a, s);
+        if (a.K > 0 && chunks <= 1024) return few ? launch_rows<T, MODE, 1024, 1>(a, s) : launch_rows<T, MODE, 256, 4>(a, s);
+        if (a.K > 0 && chunks <= 2048) return few ? launch_rows<T, MODE, 1024, 2>(a, s) : launch_rows<T, MODE, 512, 4>(a, s);
         if (a.K > 0 && chunks <= 4096) return launch_rows<T, MODE, 1024, 4>(a, s);
         hipLaunchKernelGGL((k_norm_long<T, MODE>), dim3((unsigned)(a.M < (1 << 20) ? a.M : 1 << 20)), dim3(LONG_NT),
                            0, s, a);
@@ -354,7 +382,9 @@ hipError_t launch_i8_quantize(int dtype, const NormArgs& a, hipStream_t s) { ret
 hipError_t launch_i8_dequantize(int dtype, const DequantArgs& a, hipStream_t s) {
     return with_dtype(dtype, [&](auto tag) {
         using T = typename decltype(tag)::type;
-        hipLaunchKernelGGL((k_i8_dequantize<T>), dim3((unsigned)dequantize_wgs(a)), dim3(256), 0, s, a);
+        const int per_row = (a.K + Raw<T>::N - 1) / Raw<T>::N;
+        hipLaunchKernelGGL((k_i8_dequantize<T>), dim3((unsigned)dequantize_wgs(a, per_row)), dim3(DQ_NT), 0, s, a,
+                           per_row);
         return hipGetLastError();
     });
 }

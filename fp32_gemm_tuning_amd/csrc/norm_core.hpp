@@ -8,6 +8,13 @@ namespace sgemm {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+// A value rounded to FP32 before it is rounded to a type. (The compiler would otherwise take some
+// products and their conversion to half in one instruction, with one rounding, and others not.)
+__device__ __forceinline__ float as_f32(float v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
 // N elements of a row (16 bytes, if not said otherwise) at an address aligned to its element only, as FP32.
 template <class T, int N_ = 16 / (int)sizeof(T)>
 struct Chunk {
@@ -43,7 +50,7 @@ struct Chunk {
 
 // The same 16 bytes as they are stored, for rows that stay in registers. Where a chunk would reach past the row's
 // end, the row's last 16 bytes are taken instead (`place_of`): their first elements are another lane's too, so sums
-// leave them out (`mine`), while both lanes store the same results there. No load or store is then apart from
+// leave them out (`first`), while both lanes store the same results there. No load or store is then apart from
 // the others. Rows of less than 16 bytes (SHORT) are one lane's, element by element.
 template <class T>
 struct Raw {
@@ -56,8 +63,13 @@ struct Raw {
     __device__ __forceinline__ static uint32_t place_of(int at, int n) {
         return SHORT ? 0 : (uint32_t)(at < n - N ? at : n - N);
     }
-    // Whether element e of the chunk at `place`, meant to be at `at`, is this lane's.
-    __device__ __forceinline__ static bool mine(int at, uint32_t place, int e) { return (int)place + e >= at; }
+    // The first element of the chunk at `place`, meant to be at `at`, that is this lane's. (Computed
+    // anew for each row: the compiler would otherwise keep one mask for each element of a chunk.)
+    __device__ __forceinline__ static int first(int at, uint32_t place) {
+        int k = at - (int)place;
+        asm volatile("" : "+v"(k));
+        return k;
+    }
     template <bool SHORT>
     __device__ __forceinline__ void load(const T* row, uint32_t place, int n) {
         if constexpr (!SHORT) {
