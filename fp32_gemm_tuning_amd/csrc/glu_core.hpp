@@ -637,6 +637,7 @@ template <int BM_, int BN_, int WM_, int WN_, int KS_, bool DMA_, bool SHORT_ = 
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, NT = (BM_ / WM_) * (BN_ / WN_) * KS_ * 64;
     static constexpr bool DMA = DMA_;
+    static constexpr bool ALONE = false;
     using Map = WaveMap<BM_, BN_, WM_, WN_, KS_>;
     template <class T, bool ARC, bool BRC, bool PAIR>
     using Core = std::conditional_t<DMA_, DmaCore<T, BM_, BN_, WM_, WN_, ARC, BRC, PAIR, KS_>,
