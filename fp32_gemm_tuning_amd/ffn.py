@@ -145,8 +145,11 @@ def _ld(t, like, dtype, rows: int, cols: int, name: str) -> int:
     """The leading dimension of a rows x cols matrix on `like`'s device."""
     if t.dtype is dtype and t.get_device() == like.get_device() and t.shape == (rows, cols):
         sr, sc = t.stride()
-        if rows > 1 and sr >= cols > 0 and (sc == 1 or cols == 1):
-            return sr
+        if sc == 1 or cols == 1:
+            if rows == 1:
+                return cols or 1
+            if rows and sr >= cols > 0:
+                return sr
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2 or t.shape != (rows, cols):

@@ -113,6 +113,8 @@ class I8(NamedTuple):
 
 def _vec(t, like, dtype, n: int, name: str) -> int:
     """The address of a contiguous vector of n elements on `like`'s device."""
+    if t.dtype is dtype and t.shape == (n,) and t.get_device() == like.get_device() and t.stride(0) == 1:
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (n,):
