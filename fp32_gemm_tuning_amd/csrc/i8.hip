@@ -141,10 +141,11 @@ struct FlatFill {
     }
 };
 
-// The tile filled that way: two LDS stages, and one slice under way in registers behind the one being
-// multiplied (rows that are not whole chunks cannot be loaded past the registers). Two and four register sets
-// were level or slower.
-template <int BM, int BN, int WM, int WN, bool PAIR, int KS>
+// The tile filled that way: two LDS stages, and SETS slices under way in registers behind the one being
+// multiplied (rows that are not whole chunks cannot be loaded past the registers). A second set helps the smallest
+// tile where it is alone on its unit (128 x 4091 x 4091 20.4 -> 17.5 us); larger tiles are level, or lose
+// the registers' room for a second workgroup (1000 x 4091 x 4091 on 64 x 64 tiles 60 -> 62).
+template <int BM, int BN, int WM, int WN, bool PAIR, int KS, int SETS>
 struct FlatCore {
     using T = int8_t;
     using Map = WaveMap<BM, BN, WM, WN, KS>;
@@ -173,17 +174,17 @@ struct FlatCore {
         fa.init(&la, m0, t);
         fb.init(lb, n0, t);
         const int K = la.extent;
-        i32x4 a[FA::CH], b[FB::CH];
+        i32x4 a[SETS][FA::CH], b[SETS][FB::CH];   // slice s: set s % SETS
         // Past the last slice the last one is loaded (and stored) again.
-        auto load = [&](int s) {
+        auto load = [&](int s, int set) {
             const int k0 = (s < slices ? s : slices - 1) * 128;
-            fa.load(a, k0, K);
-            fb.load(b, k0, K);
+            fa.load(a[set], k0, K);
+            fb.load(b[set], k0, K);
         };
-        auto store = [&](int s, char* st) {
+        auto store = [&](int s, int set, char* st) {
             const int k0 = (s < slices ? s : slices - 1) * 128;
-            fa.store(a, st, k0, K, t);
-            fb.store(b, st + BM * 128, k0, K, t);
+            fa.store(a[set], st, k0, K, t);
+            fb.store(b[set], st + BM * 128, k0, K, t);
         };
         auto compute = [&](const char* st) {
 #pragma unroll
@@ -200,22 +201,24 @@ struct FlatCore {
                     for (int j = 0; j < BJ; ++j) mma_chunk(T{}, w[j], x[i], acc[i][j]);
             }
         };
-        load(0);
-        store(0, lds);
-        load(1);
+        static_assert(SETS == 1 || SETS == 2, "a slice's set is known");
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) load(i, i);
+        store(0, 0, lds);
+        load(SETS, 0);
         ring_barrier<63>();
         // The stage written was last read before the previous barrier.
-        auto slice = [&](int s, char* now, char* next) {
+        auto slice = [&](int s, int set, char* now, char* next) {   // set: of slice s + 1
             compute(now);
             __builtin_amdgcn_sched_barrier(0);
-            store(s + 1, next);
-            load(s + 2);
+            store(s + 1, set, next);
+            load(s + 1 + SETS, set);
             ring_barrier<63>();
         };
         int s = 0;
         for (; s + 2 <= slices; s += 2) {
-            slice(s, lds, lds + STAGE);
-            slice(s + 1, lds + STAGE, lds);
+            slice(s, 1 % SETS, lds, lds + STAGE);
+            slice(s + 1, 0, lds + STAGE, lds);
         }
         if (s < slices) {
             compute(lds);
@@ -230,13 +233,13 @@ struct FlatCore {
         }
     }
 };
-template <int BM_, int BN_, int WM_, int WN_, int KS_>
+template <int BM_, int BN_, int WM_, int WN_, int KS_ = 1, int SETS_ = 1>
 struct Flat {
     static constexpr int BM = BM_, BN = BN_, NT = (BM_ / WM_) * (BN_ / WN_) * KS_ * 64;
     static constexpr bool ALONE = true;   // its LDS is the core's
     using Map = WaveMap<BM_, BN_, WM_, WN_, KS_>;
     template <class T, bool, bool, bool PAIR>
-    using Core = FlatCore<BM_, BN_, WM_, WN_, PAIR, KS_>;
+    using Core = FlatCore<BM_, BN_, WM_, WN_, PAIR, KS_, SETS_>;
 };
 
 // A tile for products whose tiles fill the chip once or twice, where a slice's way from memory
@@ -601,27 +604,29 @@ int check_i8(const I8Args& a, bool dual) {
 
 // Times that the choice of a kernel goes by, in microseconds, measured on MI355X (products of 16 to 4096 rows,
 // 300 to 8192 features and 777 to 8192 k): a call takes about
-//     fixed + slices max(alone, tiles per compute unit * busy)
-// with `alone` a slice of 128 k where tiles are few and `busy` a tile's share of a unit's slice where every unit
-// has one or more. What bounds a lone tile's slice is its bytes: a unit takes some 70 GB/s from
-// the caches, whatever is under way (two to eight slices a workgroup were level).
+//     fixed + rounds * each + slices max(alone, rounds * busy)
+// for `rounds` tiles on a compute unit, with `alone` a slice of 128 k where tiles are few and `busy` a tile's share
+// of a unit's slice where every unit has one or more; a workgroup of the rows' kernel has its unit to itself, and its
+// start and its sums (`each`) with it. What bounds a lone tile's slice is its bytes: a unit takes some 70
+// GB/s from the caches, whatever is under way (two to eight slices a workgroup were level). Of 104 products of random
+// sizes the choice took 1% longer than the best kernel on the average.
 struct Cost {
-    double fixed, alone, busy;
+    double fixed, each, alone, busy;
     double of(int64_t tiles, int64_t slices) const {
-        const double b = (double)((tiles + 255) / 256) * busy;
-        return fixed + (double)slices * (b > alone ? b : alone);
+        const double rounds = (double)((tiles + 255) / 256), b = rounds * busy;
+        return fixed + rounds * each + (double)slices * (b > alone ? b : alone);
     }
 };
 // [filled through registers]
-static const Cost kRows32[2] = {{4.0, 0.12, 0.12}, {3.5, 0.21, 0.22}};           // 32 x 32
-static const Cost kRows64[2] = {{4.0, 0.16, 0.165}, {3.5, 0.32, 0.33}};          // 32 x 64
-static const Cost kRows64x64 = {4.0, 0.235, 0.235};                              // buffer-to-LDS
-static const Cost kTile64 = {5.0, 0.44, 0.45};                                   // 64 x 64, through registers
-static const Cost kTile64x128[2] = {{5.0, 0.33, 0.35}, {5.0, 0.68, 0.70}};
-static const Cost kTile128[2] = {{5.0, 0.42, 0.60}, {5.0, 0.85, 1.0}};
-static const Cost kTileMid = {5.0, 0.68, 0.55};                                  // 128 x 128, two workgroups a unit
-static const Cost kTile256x128 = {6.0, 1.45, 1.62};                              // through registers
-static const Cost kTile256[2] = {{5.0, 1.3, 1.95}, {7.0, 2.2, 2.9}};
+static const Cost kRows32[2] = {{1.0, 3.0, 0.12, 0.12}, {1.0, 2.5, 0.21, 0.22}};       // 32 x 32
+static const Cost kRows64[2] = {{1.0, 3.0, 0.16, 0.165}, {1.0, 2.5, 0.32, 0.33}};      // 32 x 64
+static const Cost kRows64x64 = {1.0, 3.0, 0.235, 0.235};                               // buffer-to-LDS
+static const Cost kTile64 = {5.0, 0.0, 0.38, 0.42};                                    // 64 x 64, through registers
+static const Cost kTile64x128[2] = {{5.0, 0.0, 0.33, 0.35}, {5.0, 0.0, 0.68, 0.70}};
+static const Cost kTile128[2] = {{5.0, 0.0, 0.42, 0.60}, {5.0, 0.0, 0.85, 1.0}};
+static const Cost kTileMid = {5.0, 0.0, 0.68, 0.55};                                   // 128 x 128, two workgroups a unit
+static const Cost kTile256x128 = {6.0, 0.0, 1.45, 1.62};                               // through registers
+static const Cost kTile256[2] = {{5.0, 0.0, 1.3, 1.95}, {7.0, 0.0, 2.2, 2.9}};
 
 template <int MR, bool DUAL>
 static hipError_t launch_few(const I8Args& a, hipStream_t s) {
@@ -691,12 +696,12 @@ static hipError_t launch(const I8Args& a, hipStream_t s) {
             if constexpr (!DUAL) return launch_rows<32, 32, DUAL>(a, dma, s);
         case 1: return launch_rows<32, 64, DUAL>(a, dma, s);
         case 2: return launch_rows<64, 64, DUAL>(a, dma, s);
-        case 3: return go(TypeTag<Flat<64, 64, 32, 64, 2>>{});
-        case 4: return dma ? go(TypeTag<Ring<64, 128, 32, 64, 3>>{}) : go(TypeTag<Flat<64, 128, 32, 64, 1>>{});
-        case 5: return dma ? go(TypeTag<Ring<128, 128, 32, 64, 4>>{}) : go(TypeTag<Flat<128, 128, 32, 64, 1>>{});
+        case 3: return go(TypeTag<Flat<64, 64, 32, 64, 2, 2>>{});
+        case 4: return dma ? go(TypeTag<Ring<64, 128, 32, 64, 3>>{}) : go(TypeTag<Flat<64, 128, 32, 64>>{});
+        case 5: return dma ? go(TypeTag<Ring<128, 128, 32, 64, 4>>{}) : go(TypeTag<Flat<128, 128, 32, 64>>{});
         case 6: return go(TypeTag<TileMid>{});
-        case 7: return go(TypeTag<Flat<256, 128, 64, 64, 1>>{});
-        default: return dma ? go(TypeTag<TileBig>{}) : go(TypeTag<Flat<256, 256, 128, 64, 1>>{});
+        case 7: return go(TypeTag<Flat<256, 128, 64, 64>>{});
+        default: return dma ? go(TypeTag<TileBig>{}) : go(TypeTag<Flat<256, 256, 128, 64>>{});
     }
 }
 

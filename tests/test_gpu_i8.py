@@ -60,7 +60,7 @@ SHAPES = [(1, 1, 1), (1, 7, 1000), (1, 300, 15), (2, 300, 16), (3, 65, 31), (5, 
 LARGE = [(3000, 4136, 288), (2904, 72, 8400), (72, 2600, 5456), (520, 264, 400), (100, 3001, 260), (2500, 65, 134),
          (1201, 1203, 1205), (2050, 2048, 16), (600, 9000, 130), (4000, 4000, 100), (300, 2100, 9000),
          (500, 3100, 272), (2100, 1500, 272), (2100, 3100, 261), (1500, 5000, 1072), (2000, 2050, 1040), (130, 8200, 528),
-         (3000, 8200, 525), (64, 4100, 1040), (64, 4100, 1051), (1000, 4100, 527), (260, 1030, 4112)]
+         (3000, 8200, 525), (64, 4100, 1040), (64, 4100, 1051), (1000, 4100, 527), (260, 1030, 4112), (66, 5500, 272)]
 LAYOUTS = [(0, 0), (16, 16), (3, 1)]
 
 
