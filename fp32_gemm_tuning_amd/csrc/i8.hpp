@@ -65,7 +65,6 @@ int check_i8_dequantize(const DequantArgs& a);
 hipError_t launch_i8_dequantize(int dtype, const DequantArgs& a, hipStream_t s);
 // norm_bwd.hip
 size_t norm_part_bytes(int dtype, int64_t M, int64_t K);
-int check_norm_bwd(const NormBwdArgs& a);
 hipError_t launch_norm_bwd(int dtype, const NormBwdArgs& a, hipStream_t s);
 // i8.hip
 int check_i8(const I8Args& a, bool dual);

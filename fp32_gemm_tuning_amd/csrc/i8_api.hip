@@ -146,11 +146,9 @@ SGEMM_F32_API int sgemm_f32_rms_norm_bwd(int dtype, int64_t M, int64_t K, const 
     if (workspace_bytes > 0 && (workspace == nullptr || misaligned(workspace, 16))) return -16;
     if (!want_x && !want_w) return 0;
     if (too_large(M, 0, K)) return SGEMM_F32_ERR_TOO_LARGE;
-    if (M > 0 && workspace_bytes < norm_part_bytes(dtype, M, K)) return SGEMM_F32_ERR_WORKSPACE;
+    if (want_w && M > 0 && workspace_bytes < norm_part_bytes(dtype, M, K)) return SGEMM_F32_ERR_WORKSPACE;
     const NormBwdArgs a = {dY, W, H, rstd, dH, want_x ? dX : nullptr, want_w ? dW : nullptr, (float*)workspace,
                            lddy, ldh, lddh, lddx, (int32_t)M, (int32_t)K};
-    rc = check_norm_bwd(a);
-    if (rc) return rc;
     return status(launch_norm_bwd(dtype, a, reinterpret_cast<hipStream_t>(stream)));
 }
 

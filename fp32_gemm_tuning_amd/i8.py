@@ -182,7 +182,7 @@ def rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, workspace=None,
     reaches H otherwise (of the residual stream behind the norm), added to dX. Each of the two is
     written where a tensor is given (dX may be dH or dY), allocated where it is None, and
     left out (None in the result) where it is False. `workspace`: a CUDA tensor of at least
-    rms_norm_backward_workspace() bytes."""
+    rms_norm_backward_workspace() bytes (any, where dW is left out)."""
     d = _gpu(H, "H")
     stream = _checked(stream, H.device)
     M, K = H.shape
@@ -191,8 +191,8 @@ def rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, workspace=None,
         dX = _new(H, M, K, stream)
     if dW is None:
         dW = _new(H, K, None, stream)
-    need = rms_norm_backward_workspace(H)
     if workspace is None:
+        need = 0 if dW is False else rms_norm_backward_workspace(H)
         workspace = _new(H, need, None, stream, torch.uint8, returned=False)
     elif workspace.device != H.device:
         raise ValueError(f"workspace is on {workspace.device}, not on {H.device}")

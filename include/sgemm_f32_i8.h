@@ -31,16 +31,17 @@
  *   Y[m][f] = Sx[m] * Sw[f] * sum_k qx[m][k] * qw[f][k]     (sgemm_f32_i8)
  *   H = act(X Wg^T) * (X Wu^T), all three in 8 bits         (sgemm_f32_i8_glu)
  *
- * Sums of products are exact in 32 bits, so they do not depend on the order:
- * -128 is allowed as a stored number, and K is at most 131071
- * (SGEMM_F32_ERR_TOO_LARGE beyond).
+ * Sums of products are exact in 32 bits, so they do not depend on the order, nor a row's
+ * results on the rows beside it: -128 is allowed as a stored number, and K is at most 131071
+ * (SGEMM_F32_ERR_TOO_LARGE beyond). A sum is rounded to FP32 and multiplied by its two scales,
+ * a rounding each; only the result has to lie in FP32's range, not what is between.
  *
  * Types. `dtype` is the type of every activation, norm weight, output and gradient
  * of a call: FP32, bfloat16 or IEEE half. Scales and rstd are FP32, and the stored numbers
  * int8. H is rounded to the type, and everything after it uses the rounded one, so that the
  * backward pass sees what the forward pass did. Sums over a row or over rows are held in FP32
- * (squares beyond its range are summed times a power of two); each output is
- * rounded once from FP32.
+ * (squares next to the ends of its range are summed times a power of two); each output is
+ * rounded to the type once, from FP32.
  *
  * Infinities and NaN stay in their rows (dW: in their columns): a row of H that holds an infinity has
  * rstd = 0, and Y = 0 but for the infinity, where it is NaN; one that holds NaN is NaN. With eps = 0 a row
@@ -108,7 +109,8 @@ SGEMM_F32_API int sgemm_f32_rms_norm_i8(int dtype, int64_t M, int64_t K, float e
 /* The gradients of sgemm_f32_rms_norm for dY (M x K), from H, W and rstd. dH
  * (M x K), the gradient that reaches H from behind, may be NULL (none). dX (M x K) and
  * dW (K) are overwritten; each may be NULL, and is then not computed. The
- * workspace holds partial sums of dW (sgemm_f32_rms_norm_bwd_ws_size). */
+ * workspace holds partial sums of dW (sgemm_f32_rms_norm_bwd_ws_size); without
+ * dW none is needed. */
 SGEMM_F32_API int sgemm_f32_rms_norm_bwd(int dtype, int64_t M, int64_t K, const void *dY, int64_t lddy,
                                          const void *W, const void *H, int64_t ldh, const float *rstd,
                                          const void *dH, int64_t lddh, void *dX, int64_t lddx, void *dW,
