@@ -6,9 +6,10 @@
 
 namespace sgemm {
 
-// A scale as mantissa and exponent: sum * Sx * Sw then leaves FP32's range, or its
+// A scale as mantissa and exponent: sum * (Sx * Sw) then leaves FP32's range, or its
 // normal numbers, only where the result does (Sx = 2^-100, Sw = 2^90 and the other
-// way round are ordinary).
+// way round are ordinary). Of scales that are `plain` the product of the FP32 numbers
+// has the same bits, for two instructions less.
 struct Scale {
     float m;
     int e;
@@ -16,17 +17,37 @@ struct Scale {
     __device__ __forceinline__ explicit Scale(float s)
         : m(__builtin_amdgcn_frexp_mantf(s)), e(__builtin_amdgcn_frexp_expf(s)) {}
 };
-__device__ __forceinline__ float scaled(int sum, const Scale& x, float wm, int we) {
-    return __builtin_amdgcn_ldexpf((float)sum * x.m * wm, x.e + we);
+__device__ __forceinline__ float scaled(int sum, const Scale& x, const Scale& w) {
+    return __builtin_amdgcn_ldexpf((float)sum * (x.m * w.m), x.e + w.e);
 }
-__device__ __forceinline__ float scaled(int sum, const Scale& x, const Scale& w) { return scaled(sum, x, w.m, w.e); }
-// LDS that a wave's results go out through (put_i8): 32 rows of 64 FP32 values, and their scales.
-constexpr int STAGING = RowsOut<float, 64>::BYTES + 512;
+__device__ __forceinline__ bool plain(float s) {
+    const float a = fabsf(s);
+    return a == 0.0f || (a >= 0x1p-60f && a <= 0x1p60f);
+}
+template <bool PLAIN>
+__device__ __forceinline__ float scaled(int sum, float x, float w) {
+    if constexpr (PLAIN) return (float)sum * (x * w);
+    return scaled(sum, Scale(x), Scale(w));
+}
 
-// The gate of the call's type: 16-bit results take the hardware's exponential.
-template <class O>
-__device__ __forceinline__ float gated(int act, float g, float u) {
-    return as_f32(act_value<sizeof(O) == 4>(act, g) * u);
+// LDS that a wave's results go out through (put_i8): 32 rows of 64 FP32 values, and their scales.
+constexpr int STAGING = RowsOut<float, 64>::BYTES + 256;
+
+// g = act(g) * u, for N results with one branch (one for each result, between their instructions, took the
+// epilogue of a tile a third longer). 16-bit results take the hardware's exponential.
+template <class O, int N>
+__device__ __forceinline__ void gate(int act, float (&g)[N], const float (&u)[N]) {
+    auto all = [&](auto kind) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) g[e] = as_f32(act_value<sizeof(O) == 4>(decltype(kind)::value, g[e]) * u[e]);
+    };
+    using std::integral_constant;
+    switch (act) {
+        case SGEMM_F32_ACT_SILU: all(integral_constant<int, SGEMM_F32_ACT_SILU>{}); break;
+        case SGEMM_F32_ACT_GELU: all(integral_constant<int, SGEMM_F32_ACT_GELU>{}); break;
+        case SGEMM_F32_ACT_GELU_TANH: all(integral_constant<int, SGEMM_F32_ACT_GELU_TANH>{}); break;
+        default: all(integral_constant<int, SGEMM_F32_ACT_RELU>{});
+    }
 }
 
 // A tile's results: blocks of 32 rows of 32 (KS = 2: 16) features, or, without a gate, of all the
@@ -41,16 +62,16 @@ __device__ __forceinline__ void put_i8(const I8Args& a, char* own, int m0, int n
     constexpr int TOGETHER = DUAL ? 1 : STEP, COLS = 2 * REGS * TOGETHER;
     static_assert(Core::BJ == 2, "64 columns a wave");
     const RowsOut<O, COLS> o = {own, map.lane};
-    static_assert(RowsOut<O, COLS>::BYTES + 512 <= Core::PER_WAVE && Core::PER_WAVE % 16 == 0, "staging");
-    float* const wm = (float*)(own + Core::PER_WAVE - 512);
-    int* const we = (int*)(own + Core::PER_WAVE - 256);
+    static_assert(RowsOut<O, COLS>::BYTES + 256 <= Core::PER_WAVE && Core::PER_WAVE % 16 == 0, "staging");
+    float* const scales = (float*)(own + Core::PER_WAVE - 256);
     const int f0 = n0 + (DUAL ? map.wn >> 1 : map.wn);
+    bool all_plain;
     {
         const int c = f0 + (DUAL ? map.lane & 31 : map.lane);
         const float* sw = DUAL && map.lane >= 32 ? a.Sw[1] : a.Sw[0];
-        const Scale mine(sw[c < a.F ? c : a.F - 1]);
-        wm[map.lane] = mine.m;
-        we[map.lane] = mine.e;
+        const float mine = sw[c < a.F ? c : a.F - 1];
+        scales[map.lane] = mine;
+        all_plain = __builtin_amdgcn_ballot_w64(!plain(mine)) == 0;
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
@@ -58,33 +79,38 @@ __device__ __forceinline__ void put_i8(const I8Args& a, char* own, int m0, int n
 #pragma unroll
     for (int bi = 0; bi < Core::BI; ++bi) {
         const int row = m0 + map.wm + 32 * bi, mine = row + (map.lane & 31);
-        const Scale sx(a.Sx[mine < a.M ? mine : a.M - 1]);
+        const float sx = a.Sx[mine < a.M ? mine : a.M - 1];
+        auto blocks = [&](auto is_plain) {
+            constexpr bool PLAIN = decltype(is_plain)::value;
 #pragma unroll
-        for (int bj = 0; bj < Core::BJ; bj += STEP) {
-            const int col = (DUAL ? 0 : 32 * bj) + 2 * REGS * map.kk;   // of the wave's
+            for (int bj = 0; bj < Core::BJ; bj += STEP) {
+                const int col = (DUAL ? 0 : 32 * bj) + 2 * REGS * map.kk;   // of the wave's
 #pragma unroll
-            for (int j = 0; j < TOGETHER; ++j)
+                for (int j = 0; j < TOGETHER; ++j) {
+                    float g[REGS], u[REGS];
 #pragma unroll
-                for (int r = 0; r < REGS; r += 4) {
-                    const int at = col + 32 * j + 2 * r + half;
-                    const f32x4 gm = *(const f32x4*)(wm + at);
-                    const i32x4 ge = *(const i32x4*)(we + at);
-                    float v[4];
-                    if constexpr (DUAL) {
-                        const f32x4 um = *(const f32x4*)(wm + 32 + at);
-                        const i32x4 ue = *(const i32x4*)(we + 32 + at);
+                    for (int r = 0; r < REGS; r += 4) {
+                        const int at = col + 32 * j + 2 * r + half;
+                        const f32x4 sg = *(const f32x4*)(scales + at);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = gated<O>(a.act, scaled(acc[bi][bj][r + e], sx, gm[e], ge[e]),
-                                            scaled(acc[bi][bj + 1][r + e], sx, um[e], ue[e]));
-                    } else {
+                        for (int e = 0; e < 4; ++e) g[r + e] = scaled<PLAIN>(acc[bi][bj + j][r + e], sx, sg[e]);
+                        if constexpr (DUAL) {
+                            const f32x4 su = *(const f32x4*)(scales + 32 + at);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = scaled(acc[bi][bj + j][r + e], sx, gm[e], ge[e]);
+                            for (int e = 0; e < 4; ++e) u[r + e] = scaled<PLAIN>(acc[bi][bj + 1][r + e], sx, su[e]);
+                        }
                     }
-                    o.put(32 * j + 2 * r, v[0], v[1], v[2], v[3]);
+                    if constexpr (DUAL) gate<O>(a.act, g, u);
+#pragma unroll
+                    for (int r = 0; r < REGS; r += 4) o.put(32 * j + 2 * r, g[r], g[r + 1], g[r + 2], g[r + 3]);
                 }
-            o.flush((O*)a.Y + f0 + col, a.ldy, row, a.M, a.F - f0 - col);
-        }
+                o.flush((O*)a.Y + f0 + col, a.ldy, row, a.M, a.F - f0 - col);
+            }
+        };
+        if (all_plain && __builtin_amdgcn_ballot_w64(!plain(sx)) == 0)
+            blocks(std::true_type{});
+        else
+            blocks(std::false_type{});
     }
 }
 
@@ -438,11 +464,12 @@ __global__ __launch_bounds__(256) void k_i8_few(I8Args a) {
     if (m < MR && m0 + m < a.M && f0 + f < a.F) {
         auto sum = [&](int i) { return red[0][m][i] + red[1][m][i] + red[2][m][i] + red[3][m][i]; };
         const Scale sx(a.Sx[m0 + m]);
-        const float g = scaled(sum(f), sx, Scale(a.Sw[0][f0 + f]));
-        const float u = DUAL ? scaled(sum(2 + f), sx, Scale(a.Sw[1][f0 + f])) : 0.0f;
+        float g[1] = {scaled(sum(f), sx, Scale(a.Sw[0][f0 + f]))};
+        const float u[1] = {DUAL ? scaled(sum(2 + f), sx, Scale(a.Sw[1][f0 + f])) : 0.0f};
         with_out(a, [&](auto* o) {
             using O = std::remove_pointer_t<decltype(o)>;
-            ((O*)a.Y)[(int64_t)(m0 + m) * a.ldy + f0 + f] = (O)(DUAL ? gated<O>(a.act, g, u) : g);
+            if constexpr (DUAL) gate<O>(a.act, g, u);
+            ((O*)a.Y)[(int64_t)(m0 + m) * a.ldy + f0 + f] = (O)g[0];
         });
     }
 }
@@ -544,7 +571,7 @@ __global__ __launch_bounds__(KW * 64) void k_i8_rows(I8Args a) {
     __syncthreads();
     // Each wave a share of the registers: lane l holds feature l % 32 of rows 8 (r / 4) + 4 (l / 32) + r % 4.
     constexpr int MINE = BI * 16 / KW;
-    float g[MINE][OUTS], u[MINE][OUTS];
+    float g[MINE * OUTS], u[MINE * OUTS];
     auto row_of = [&](int o) {
         const int ir = w * MINE + o, r = ir & 15;
         return m0 + 32 * (ir >> 4) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
@@ -568,19 +595,19 @@ __global__ __launch_bounds__(KW * 64) void k_i8_rows(I8Args a) {
         };
 #pragma unroll
         for (int j = 0; j < OUTS; ++j) {
-            g[o][j] = scaled(sum(DUAL ? 2 * j : j), sx, sw[0][j]);
-            if (DUAL) u[o][j] = scaled(sum(2 * j + 1), sx, sw[DUAL ? 1 : 0][j]);
+            g[o * OUTS + j] = scaled(sum(DUAL ? 2 * j : j), sx, sw[0][j]);
+            if (DUAL) u[o * OUTS + j] = scaled(sum(2 * j + 1), sx, sw[DUAL ? 1 : 0][j]);
         }
     }
     with_out(a, [&](auto* out) {
         using O = std::remove_pointer_t<decltype(out)>;
+        if constexpr (DUAL) gate<O>(a.act, g, u);
 #pragma unroll
         for (int o = 0; o < MINE; ++o)
 #pragma unroll
             for (int j = 0; j < OUTS; ++j) {
                 const int row = row_of(o), f = f0 + 32 * j + (lane & 31);
-                if (row < a.M && f < a.F)
-                    ((O*)a.Y)[(int64_t)row * a.ldy + f] = (O)(DUAL ? gated<O>(a.act, g[o][j], u[o][j]) : g[o][j]);
+                if (row < a.M && f < a.F) ((O*)a.Y)[(int64_t)row * a.ldy + f] = (O)g[o * OUTS + j];
             }
     });
 }
