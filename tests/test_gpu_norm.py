@@ -381,6 +381,40 @@ def test_outputs_in_place_of_inputs(dev, dtype, K):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("K", [5, 100, 3000, 20000, 70001])
+@pytest.mark.parametrize("dtype", ref.DTYPES)
+def test_unusual_rows_in_place(dev, dtype, K):
+    # The rows that are read again for each pass, written over their inputs: as when written elsewhere.
+    t = ref.DTYPES[dtype]
+    _say("unusual in place", dtype, K)
+    X, R, W = _inputs((8, K), t, dev, 16)
+    big, small = (30000.0, 2e-7) if dtype == "f16" else (2e38, 1e-38)
+    for v in (X, R):
+        v[1] = 0
+        v[2, K // 2] = float("inf")
+        v[3, 0] = float("nan")
+        v[4] = (v[4].double().clamp(-0.4, 0.4) * big).to(t)
+        v[5] = (v[5].double() * small).to(t)
+    for eps in (1e-5, 0.0):
+        y, h = torch.empty_like(X), torch.empty_like(X)
+        sg.rms_norm(X, W, eps, residual=R, out=y, total=h)
+        q = sg.rms_norm_i8(X, W, eps, residual=R)
+        same = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))   # noqa: E731 (NaN alike)
+        for first in (True, False):
+            x2, r2 = X.clone(), R.clone()
+            mine, other = (x2, r2) if first else (r2, x2)
+            sg.rms_norm(x2, W, eps, residual=r2, total=other, out=mine)
+            assert same(mine, y) and same(other, h)
+            x2, r2 = X.clone(), R.clone()
+            mine = x2 if first else r2
+            sg.rms_norm(x2, W, eps, residual=r2, out=mine)
+            assert same(mine, y)
+            x2, r2 = X.clone(), R.clone()
+            mine = x2 if first else r2
+            p = sg.rms_norm_i8(x2, W, eps, residual=r2, total=mine)
+            assert same(p.q, q.q) and same(p.scales, q.scales) and same(mine, h)
+
+
 @pytest.mark.parametrize("dtype", ref.DTYPES)
 def test_offsets_past_32_bits(dev, dtype):
     # Three rows of 2^31 elements and more apart, of which only their first ones are touched.
