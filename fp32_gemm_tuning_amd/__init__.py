@@ -46,6 +46,10 @@ The gated feed-forward block, its backward pass and products with 4-bit
 weights (float32, bfloat16, float16; include/sgemm_f32_ffn.h) are bound in
 ffn.py and exported here: glu, glu_backward, w4_quantize, w4_dequantize,
 w4_matmul, w4_glu, and the sgemm_f32_glu* and sgemm_f32_w4* mirrors.
+The root-mean-square norm, its backward pass, and products of matrices in 8 bits
+(include/sgemm_f32_i8.h) are bound in i8.py: rms_norm, rms_norm_backward,
+rms_norm_i8, i8_quantize, i8_dequantize, i8_matmul, i8_glu, and the
+sgemm_f32_rms_norm* and sgemm_f32_i8* mirrors.
 """
 from __future__ import annotations
 
