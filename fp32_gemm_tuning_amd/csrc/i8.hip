@@ -709,9 +709,11 @@ static hipError_t launch(const I8Args& a, hipStream_t s) {
         }
     };
     const int reg = !dma;
-    if (!DUAL) offer(0, kRows32[reg], 32, 32);
-    offer(1, kRows64[reg], 32, 64);
-    if (dma) offer(2, kRows64x64, 64, 64);
+    if (cdiv(a.M, 32) <= 65535) {   // their blocks of rows are the grid's second extent
+        if (!DUAL) offer(0, kRows32[reg], 32, 32);
+        offer(1, kRows64[reg], 32, 64);
+        if (dma) offer(2, kRows64x64, 64, 64);
+    }
     if (!dma) offer(3, kTile64, 64, 64);
     offer(4, kTile64x128[reg], 64, 128);
     offer(5, kTile128[reg], 128, 128);

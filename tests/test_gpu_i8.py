@@ -218,6 +218,26 @@ def test_offsets_past_32_bits(dev):
         del fa, fb, y
 
 
+def test_more_rows_of_blocks_than_a_second_grid_extent(dev):
+    # 65537 blocks of 64 rows of few features and a long sum, where the rows' kernel would be the fastest.
+    _say("i8 four million rows")
+    M, F, K = 65536 * 64 + 1, 16, 10240
+    if torch.cuda.mem_get_info(dev)[0] < 48 << 30:
+        pytest.skip("less than 48 GiB of memory free")
+    gen = _gen(7)
+    rows = torch.tensor([0, 1, 63, 64, 65535 * 64 - 1, 65535 * 64, M - 2, M - 1], device=dev)
+    _, some = _matrix(len(rows), K, gen, dev)
+    _, w = _matrix(F, K, gen, dev)
+    q, scales = torch.zeros(M, K, dtype=torch.int8, device=dev), torch.ones(M, device=dev)
+    q[rows], scales[rows] = some.q, some.scales
+    got = sg.i8_matmul(sg.I8(q, scales), w)
+    assert torch.equal(got[rows], sg.i8_matmul(some, w))
+    got[rows] = 0
+    assert (got == 0).all()
+    del q
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------------------
 # As they are used together
 # ---------------------------------------------------------------------------

@@ -344,7 +344,7 @@ def test_empty_rows_and_no_rows(dev):
 # ---------------------------------------------------------------------------
 # Memory
 # ---------------------------------------------------------------------------
-@pytest.mark.parametrize("K", [100, 777, 4096, 20000, 70001])
+@pytest.mark.parametrize("K", [100, 777, 4096, 8189, 16381, 20000, 70001])
 @pytest.mark.parametrize("dtype", ref.DTYPES)
 def test_outputs_in_place_of_inputs(dev, dtype, K):
     t = ref.DTYPES[dtype]
