@@ -126,6 +126,8 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int lane,
     }
 }
 
+// Longer rows: a workgroup each, read from the caches or memory in every pass. Bound by those
+// reads: 512 x 65536 bf16 with a residual 59 us (268 MB, 4.5 TB/s), to 8 bits 76 (3.1 TB/s), one row 11 and 22.
 constexpr int LONG_NT = 1024;
 template <class T, NormMode MODE>
 __global__ __launch_bounds__(LONG_NT) void k_norm_long(NormArgs a) {
@@ -134,10 +136,9 @@ __global__ __launch_bounds__(LONG_NT) void k_norm_long(NormArgs a) {
 }
 
 // Rows that stay in registers: LANES lanes hold a row in C chunks each, part of a wave, a wave or a
-// workgroup, so that it is read once. Bound by its bytes: 4096 x 8192 bf16 with a residual 43 us (268 MB, 6.3
-// TB/s, some of it cached), 131072 x 128 f16 12 us (5.4 TB/s), in 8 bits 2047 x 4096 FP32 24 us (109 MB, 4.6 TB/s), 8192 x
-// 8192 FP32 to 8 bits 64 us (335 MB, 5.2 TB/s; one workgroup of 1024 lanes a unit, with no other row's loads
-// behind the sums, 84); one row of 4096 2.4 us. What leaves the ordinary
+// workgroup, so that it is read once. Bound by its bytes: calls back to back, 4096 x 8192 bf16 with a residual
+// take 42 us (268 MB, 6.3 TB/s, some of it cached), 131072 x 128 f16 12 (5.4 TB/s), 4096 x 8192 bf16 with a residual
+// to 8 bits 40 (235 MB, 5.8 TB/s), 8192 x 8192 FP32 to 8 bits 64 (335 MB, 5.2 TB/s), one row of 8192 bf16 2.6. What leaves the ordinary
 // (squares or products next to the ends of FP32's range, infinities, NaN) is left to norm_row, which starts
 // anew: nothing has been written by then.
 template <class T, NormMode MODE, int LANES, int C, bool SHORT>
@@ -364,8 +365,9 @@ static hipError_t launch(int dtype, const NormArgs& a, hipStream_t s) {
         constexpr int N = Raw<T>::N;
         const int chunks = (a.K + N - 1) / N;
         // Lanes by the row's chunks. Up to a workgroup a compute unit, long rows get more lanes, for the
-        // shorter way (16 x 8192 bf16 to 8 bits 2.9 us against 3.4); beyond, fewer, so that a unit holds several rows
-        // (8192 x 8192 FP32 64 us on 512 lanes, 84 on 1024).
+        // shorter way (with a residual, 16 x 8192 bf16 2.8 us on 1024 lanes and 3.2 on 256, to 8 bits 4.3 and 5.0);
+        // beyond, fewer, so that a unit holds several rows (on 512 lanes and on 1024: 300 x 8192 FP32 9.5 and 10.5,
+        // 4096 x 16384 bf16 to 8 bits 93 and 102; 8192 x 8192 FP32 level, 64 and 63 without the norm).
         const bool few = a.M <= 256;
         if (a.K > 0 && a.K < N) return launch_rows<T, MODE, 16, 1, true>(a, s);
         if (a.K > 0 && chunks <= 16) return launch_rows<T, MODE, 16, 1>(a, s);

@@ -13,8 +13,8 @@ __device__ __forceinline__ float through(float dy, float w, float n, float rstd,
 // Rows that stay in registers, as in the forward pass: LANES lanes hold a row in C chunks each. A
 // workgroup takes every gridDim.x-th row (group of rows), and each lane sums dW for its
 // columns over them, so that one read of dY and H serves both gradients; the lanes' sums of the groups of a workgroup
-// meet in LDS. Bound by its bytes (dY, H and dH read, dX written): 4096 x 8192 bf16 44 us (268
-// MB, 6.1 TB/s, some of it cached), FP32 99 (5.4 TB/s); two passes over the rows took 79. At most two chunks a
+// meet in LDS. Bound by its bytes (dY, H and dH read, dX written): 4096 x 8192 bf16 49 us in a kernel trace (268
+// MB and 17 MB of partial sums, 5.8 TB/s); one pass for dX and one for dW took 79. At most two chunks a
 // lane of 16-bit rows: their FP32 sums are twice the registers.
 // X: dX is wanted, D: with a dH.
 template <class T, int LANES, int C, bool SHORT, bool X, bool D>
@@ -122,7 +122,8 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm_bwd(NormB
     }
 }
 
-// dX of longer rows: a workgroup a row, read twice.
+// dX of longer rows: a workgroup a row, read twice. Bound by those reads: with dW's two kernels 512 x 65536 bf16 with dH
+// 100 us (268 MB without the second reads, 2.7 TB/s), one row 20.
 constexpr int LONG_NT = 1024;
 template <class T>
 __global__ __launch_bounds__(LONG_NT) void k_norm_dx_long(NormBwdArgs a) {

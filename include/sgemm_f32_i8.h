@@ -45,7 +45,7 @@
  *
  * Infinities and NaN stay in their rows (dW: in their columns): a row of H that holds an infinity has
  * rstd = 0, and Y = 0 but for the infinity, where it is NaN; one that holds NaN is NaN. With eps = 0 a row
- * of zeros has rstd = inf and Y = NaN. A scale that is infinite or NaN gives what the product of FP32
+ * of zeros has rstd = inf and Y = NaN, and one whose root mean square is below 2^-128 rstd = inf. A scale that is infinite or NaN gives what the product of FP32
  * numbers gives.
  *
  * Layout. Matrices are row-major with unit column stride and a leading
