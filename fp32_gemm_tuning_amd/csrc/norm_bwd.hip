@@ -69,6 +69,12 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm_bwd(NormB
                     }
                 }
             }
+            // dH has arrived before the barriers of the sum: dX may be written over it, and a chunk moved back from
+            // the row's end reads what another wave writes.
+            if constexpr (D && LANES > 64) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[c].forget();
+            }
             along = over_row<LANES>(along, Plus{}, red) / (float)a.K;
             if (there) {
 #pragma unroll

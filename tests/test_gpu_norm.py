@@ -381,6 +381,21 @@ def test_outputs_in_place_of_inputs(dev, dtype, K):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("K", [1027, 2051, 4099, 8195])
+@pytest.mark.parametrize("dtype", ref.DTYPES)
+def test_gradients_in_place_where_waves_share_elements(dev, dtype, K):
+    # The last chunk of 16 bytes is moved back into the one that another wave of the workgroup holds and writes.
+    t = ref.DTYPES[dtype]
+    _say("gradients in place", dtype, K)
+    H, D, W = _inputs((700, K), t, dev, 17)
+    dY, r = _normal((700, K), _gen(18, K), dev, t), torch.rand(700, device=dev) + 0.5
+    want = sg.rms_norm_backward(dY, H, W, r, dH=D)
+    for where in ("dH", "dY"):
+        d2, y2 = D.clone(), dY.clone()
+        got = sg.rms_norm_backward(y2, H, W, r, dH=d2, dX=d2 if where == "dH" else y2)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("K", [5, 100, 3000, 20000, 70001])
 @pytest.mark.parametrize("dtype", ref.DTYPES)
 def test_unusual_rows_in_place(dev, dtype, K):
