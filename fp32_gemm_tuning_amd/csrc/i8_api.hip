@@ -30,9 +30,10 @@ int check_sizes(int dtype, int64_t M, int64_t F, int64_t K) {
 bool too_large(int64_t M, int64_t F, int64_t K) { return M > kMaxExtent || F > kMaxExtent || K > kMaxExtent; }
 int status(hipError_t e) { return e == hipSuccess ? 0 : (int)e; }
 
-// What the two forms of the norm share: sizes, inputs and the sum's output.
+// What the two forms of the norm share: sizes and inputs, and, looked at after rms_norm_i8's own
+// outputs, the sum's output.
 int check_inputs(int dtype, int64_t M, int64_t K, float eps, const void* X, int64_t ldx, const void* R,
-                 int64_t ldr, const void* W, const void* H, int64_t ldh) {
+                 int64_t ldr, const void* W) {
     const int rc = check_sizes(dtype, M, 0, K);
     if (rc) return rc;
     if (!(eps >= 0.0f) || std::isinf(eps)) return -40;
@@ -43,7 +44,10 @@ int check_inputs(int dtype, int64_t M, int64_t K, float eps, const void* X, int6
     if (used && misaligned(R, e)) return -38;
     if (R != nullptr && short_ld(ldr, K)) return -39;
     if (bad_ptr(used, W, e)) return -7;
-    if (used && misaligned(H, e)) return -41;
+    return 0;
+}
+int check_total(int dtype, int64_t M, int64_t K, const void* H, int64_t ldh) {
+    if (M > 0 && K > 0 && misaligned(H, dtype_bytes(dtype))) return -41;
     if (H != nullptr && short_ld(ldh, K)) return -42;
     return 0;
 }
@@ -88,7 +92,8 @@ extern "C" {
 SGEMM_F32_API int sgemm_f32_rms_norm(int dtype, int64_t M, int64_t K, float eps, const void* X,
                                      int64_t ldx, const void* R, int64_t ldr, const void* W, void* H,
                                      int64_t ldh, float* rstd, void* Y, int64_t ldy, void* stream) {
-    int rc = check_inputs(dtype, M, K, eps, X, ldx, R, ldr, W, H, ldh);
+    int rc = check_inputs(dtype, M, K, eps, X, ldx, R, ldr, W);
+    if (rc == 0) rc = check_total(dtype, M, K, H, ldh);
     if (rc) return rc;
     if (M > 0 && misaligned(rstd, 4)) return -43;
     if (bad_ptr(M > 0 && K > 0, Y, dtype_bytes(dtype))) return -10;
@@ -102,11 +107,13 @@ SGEMM_F32_API int sgemm_f32_rms_norm(int dtype, int64_t M, int64_t K, float eps,
 SGEMM_F32_API int sgemm_f32_rms_norm_i8(int dtype, int64_t M, int64_t K, float eps, const void* X,
                                         int64_t ldx, const void* R, int64_t ldr, const void* W, void* H,
                                         int64_t ldh, int8_t* Q, int64_t ldq, float* S, void* stream) {
-    int rc = check_inputs(dtype, M, K, eps, X, ldx, R, ldr, W, H, ldh);
+    int rc = check_inputs(dtype, M, K, eps, X, ldx, R, ldr, W);
     if (rc) return rc;
     if (bad_ptr(M > 0 && K > 0, Q, 1)) return -7;
     if (short_ld(ldq, K)) return -8;
     if (bad_ptr(M > 0, S, 4)) return -32;
+    rc = check_total(dtype, M, K, H, ldh);
+    if (rc) return rc;
     if (M == 0) return 0;
     if (too_large(M, 0, K)) return SGEMM_F32_ERR_TOO_LARGE;
     const NormArgs a = {X, R, W, H, nullptr, nullptr, Q, S, ldx, ldr, ldh, 1, ldq, (int32_t)M, (int32_t)K, eps};

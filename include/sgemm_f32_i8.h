@@ -70,7 +70,7 @@
  *   -40 eps is negative, infinite or NaN
  *   -5 X        -6 ldx     -44 Sx     -38 R      -39 ldr
  *   -45 dY      -46 lddy
- *   -7 W (Wg, Q)           -8 ldw (ldwg, ldq)    -32 S (Sw, Sg)
+ *   -7 W (Wg, Q; rms_norm_i8 has both, W first)  -8 ldw (ldwg, ldq)    -32 S (Sw, Sg)
  *   -19 Wu      -20 ldwu   -36 Su
  *   -41 H (the norm's)     -42 ldh    -43 rstd
  *   -23 dH      -24 lddh
@@ -78,8 +78,8 @@
  *   -25 dX      -26 lddx   -27 dW
  *   -16 workspace NULL with a nonzero size or not 16-byte aligned
  *   -12 output pointer NULL
- *   SGEMM_F32_ERR_WORKSPACE   workspace_bytes below what the _ws_size reports
  *   SGEMM_F32_ERR_TOO_LARGE   a size exceeds what the kernels can index
+ *   SGEMM_F32_ERR_WORKSPACE   workspace_bytes below what the _ws_size reports
  * A pointer is checked (not NULL, aligned to its element) where it is read or
  * written; leading dimensions of operands that are not NULL always.
  */
