@@ -564,6 +564,14 @@ __device__ __forceinline__ void wave_wait() {
     asm volatile("" ::: "memory");
 }
 
+// Between a wave's lanes writing LDS of the wave's own and other lanes of it reading that, and before it is written
+// again. The hardware keeps a wave's LDS instructions in their order, so nothing is waited for; the
+// compiler, which sees each lane's addresses by themselves, may not move one across.
+__device__ __forceinline__ void lanes_meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // One block row of a wave's results on its way out: 32 rows of COLS columns of
 // type O, through LDS of the wave's own (no barrier), so that a store
 // instruction writes whole runs of rows, 16 bytes a lane. The matrix instructions take
@@ -586,8 +594,7 @@ struct RowsOut {
     // To rows row0 .. of a matrix whose first column here is `out`'s; `rows` and
     // `cols` of them exist.
     __device__ __forceinline__ void flush(O* out, int64_t ld, int row0, int rows, int cols) const {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
+        lanes_meet();
         typedef O E __attribute__((ext_vector_type(EPC)));
         typedef E Eu __attribute__((aligned(sizeof(O))));
 #pragma unroll
@@ -605,8 +612,7 @@ struct RowsOut {
                 }
             }
         }
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
+        lanes_meet();
     }
 };
 

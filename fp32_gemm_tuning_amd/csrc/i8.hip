@@ -74,8 +74,7 @@ __device__ __forceinline__ void put_i8(const I8Args& a, char* own, int m0, int n
         scales[map.lane] = mine;
         all_plain = __builtin_amdgcn_ballot_w64(!plain(mine)) == 0;
     }
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
+    lanes_meet();
     const int half = 4 * (map.lane >> 5);
 #pragma unroll
     for (int bi = 0; bi < Core::BI; ++bi) {
@@ -559,10 +558,12 @@ __global__ __launch_bounds__(KW * 64) void k_i8_rows(I8Args a) {
         for (int i = 0; i < count; ++i) {
             fa.store(av, ring, k_of(i), a.K, lane);
             fb.store(bv, ring + BM * 128, k_of(i), a.K, lane);
+            lanes_meet();
             const int next = k_of(i + 1 < count ? i + 1 : i);
             fa.load(av, next, a.K);
             fb.load(bv, next, a.K);
             compute(ring);
+            lanes_meet();
         }
     }
     __syncthreads();
