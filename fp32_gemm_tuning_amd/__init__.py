@@ -31,7 +31,8 @@ or raw device addresses as ints; they return the C status code):
     sgemm_f32_num_variants(), sgemm_f32_variant_name(v), sgemm_f32_variant_by_name(s),
     sgemm_f32_strerror(code), sgemm_f32_kernel_info(v) -> dict
     sgemm_f32_peak_probe(kind, workgroups, iters, out, stream=None) -> (code, flops),
-    sgemm_f32_clock_rates() -> (code, wall_khz, max_sclk_khz)   (include/sgemm_f32_probe.h)
+    sgemm_f32_clock_rates() -> (code, wall_khz, max_sclk_khz)   (include/sgemm_f32_probe.h;
+                        its sgemm_f32_i8_kernel is in i8.py)
     sgemm_f32_set_model(entries) -> code, sgemm_f32_get_model() -> list of dicts
 
 Tensor helper:
@@ -463,5 +464,5 @@ from .ffn import (ACTS, W4, glu, glu_backward, glu_backward_workspace, sgemm_f32
 # The norm before that block, and its products in 8 bits (i8.py).
 from .i8 import (I8, i8_dequantize, i8_glu, i8_matmul, i8_quantize, rms_norm, rms_norm_backward,  # noqa: E402,F401
                  rms_norm_backward_workspace, rms_norm_i8, sgemm_f32_i8, sgemm_f32_i8_dequantize,
-                 sgemm_f32_i8_glu, sgemm_f32_i8_quantize, sgemm_f32_rms_norm, sgemm_f32_rms_norm_bwd,
-                 sgemm_f32_rms_norm_bwd_ws_size, sgemm_f32_rms_norm_i8)
+                 sgemm_f32_i8_glu, sgemm_f32_i8_kernel, sgemm_f32_i8_quantize, sgemm_f32_rms_norm,
+                 sgemm_f32_rms_norm_bwd, sgemm_f32_rms_norm_bwd_ws_size, sgemm_f32_rms_norm_i8)

@@ -680,6 +680,74 @@ static hipError_t launch_rows(const I8Args& a, bool dma, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The kernel of a call, and whether it is filled by buffer-to-LDS loads.
+enum I8Kernel { FEW1, FEW2, FEW4, FEW8, ROWS32, ROWS64, ROWS64X64, TILE64, TILE64X128, TILE128, TILE_MID, TILE256X128,
+                TILE256, TILE_SHORT, TILE_FAR };
+struct I8Choice {
+    I8Kernel kernel;
+    bool dma;
+};
+
+static I8Choice choose(const I8Args& a, bool dual) {
+    const bool dma = dma_ok(1, a.X, a.ldx, a.K, 256) && dma_ok(1, a.W[0], a.ldw[0], a.K, 256) &&
+                     (!dual || dma_ok(1, a.W[1], a.ldw[1], a.K, 256));
+    if (a.K < Elem<int8_t>::EPC) return {TILE_SHORT, false};
+    const int64_t slices = cdiv(a.K, Elem<int8_t>::SLICE), cols = (dual ? 2 : 1) * (int64_t)a.F;
+    // Very few rows, or few features: the vector units (in us, here against the rows' kernel: one row of
+    // 8192 x 8192 12.3 and 16.7, eight 18.4 and 17.8, gated four 26.6 and 27.8, eight 33 and 27; 16
+    // rows of 300 x 4096 3.6 and 5.7, of 1000 x 4096 5.0 and 5.9, 32 rows 6.4 and 6.2).
+    if (cdiv(a.F, 2) <= max_workgroups(256) &&
+        (a.M <= (dual ? 4 : 8) || (a.M <= 32 && cdiv(a.M, 8) * cols <= 4096)))
+        return {a.M <= 1 ? FEW1 : a.M <= 2 ? FEW2 : a.M <= 4 ? FEW4 : FEW8, false};
+    // Rows too far apart for offsets of 32 bits within a tile: 64-bit addresses.
+    const int64_t far = (int64_t)kRange / 256;
+    if (a.ldx >= far || a.ldw[0] >= far || (dual && a.ldw[1] >= far)) return {TILE_FAR, false};
+    I8Kernel best = TILE256;
+    double least = -1.0;
+    auto offer = [&](I8Kernel id, const Cost& c, int64_t bm, int64_t bn) {
+        const double t = c.of(cdiv(a.M, bm) * cdiv(cols, bn), slices);
+        if (least < 0.0 || t < least) {
+            best = id;
+            least = t;
+        }
+    };
+    const int reg = !dma;
+    if (cdiv(a.M, 32) <= 65535) {   // their blocks of rows are the grid's second extent
+        if (!dual) offer(ROWS32, kRows32[reg], 32, 32);
+        offer(ROWS64, kRows64[reg], 32, 64);
+        if (dma) offer(ROWS64X64, kRows64x64, 64, 64);
+    }
+    if (!dma) offer(TILE64, kTile64, 64, 64);
+    offer(TILE64X128, kTile64x128[reg], 64, 128);
+    offer(TILE128, kTile128[reg], 128, 128);
+    if (dma) offer(TILE_MID, kTileMid, 128, 128);
+    if (!dma) offer(TILE256X128, kTile256x128, 256, 128);
+    offer(TILE256, kTile256[reg], 256, 256);
+    return {best, dma};
+}
+
+const char* i8_kernel_name(const I8Args& a, bool dual) {
+    if (a.K == 0) return "zero";
+    const I8Choice c = choose(a, dual);
+    switch (c.kernel) {
+        case FEW1: return "few 1";
+        case FEW2: return "few 2";
+        case FEW4: return "few 4";
+        case FEW8: return "few 8";
+        case ROWS32: return c.dma ? "rows 32x32" : "rows 32x32 through registers";
+        case ROWS64: return c.dma ? "rows 32x64" : "rows 32x64 through registers";
+        case ROWS64X64: return "rows 64x64";
+        case TILE64: return "flat 64x64";
+        case TILE64X128: return c.dma ? "ring 64x128" : "flat 64x128";
+        case TILE128: return c.dma ? "ring 128x128" : "flat 128x128";
+        case TILE_MID: return "tile 128x128";
+        case TILE256X128: return "flat 256x128";
+        case TILE256: return c.dma ? "tile 256x256" : "flat 256x256";
+        case TILE_SHORT: return "tile 128x128 of short rows";
+        default: return "tile 64x64 of far rows";
+    }
+}
+
 template <bool DUAL>
 static hipError_t launch(const I8Args& a, hipStream_t s) {
     auto go = [&](auto tile) {
@@ -689,55 +757,24 @@ static hipError_t launch(const I8Args& a, hipStream_t s) {
                            xcd_remap_enabled());
         return hipGetLastError();
     };
-    const bool dma = dma_ok(1, a.X, a.ldx, a.K, 256) && dma_ok(1, a.W[0], a.ldw[0], a.K, 256) &&
-                     (!DUAL || dma_ok(1, a.W[1], a.ldw[1], a.K, 256));
-    if (a.K < Elem<int8_t>::EPC) return go(TypeTag<TileShort>{});
-    const int64_t slices = cdiv(a.K, Elem<int8_t>::SLICE), cols = (DUAL ? 2 : 1) * (int64_t)a.F;
-    // Very few rows, or few features: the vector units (in us, here against the rows' kernel: one row of
-    // 8192 x 8192 12.3 and 16.7, eight 18.4 and 17.8, gated four 26.6 and 27.8, eight 33 and 27; 16
-    // rows of 300 x 4096 3.6 and 5.7, of 1000 x 4096 5.0 and 5.9, 32 rows 6.4 and 6.2).
-    if (cdiv(a.F, 2) <= max_workgroups(256) &&
-        (a.M <= (DUAL ? 4 : 8) || (a.M <= 32 && cdiv(a.M, 8) * cols <= 4096))) {
-        if (a.M <= 1) return launch_few<1, DUAL>(a, s);
-        if (a.M <= 2) return launch_few<2, DUAL>(a, s);
-        if (a.M <= 4) return launch_few<4, DUAL>(a, s);
-        return launch_few<8, DUAL>(a, s);
-    }
-    // Rows too far apart for offsets of 32 bits within a tile: 64-bit addresses.
-    const int64_t far = (int64_t)kRange / 256;
-    if (a.ldx >= far || a.ldw[0] >= far || (DUAL && a.ldw[1] >= far)) return go(TypeTag<TileReg64>{});
-    int best = -1;
-    double least = 0.0;
-    auto offer = [&](int id, const Cost& c, int64_t bm, int64_t bn) {
-        const double t = c.of(cdiv(a.M, bm) * cdiv(cols, bn), slices);
-        if (best < 0 || t < least) {
-            best = id;
-            least = t;
-        }
-    };
-    const int reg = !dma;
-    if (cdiv(a.M, 32) <= 65535) {   // their blocks of rows are the grid's second extent
-        if (!DUAL) offer(0, kRows32[reg], 32, 32);
-        offer(1, kRows64[reg], 32, 64);
-        if (dma) offer(2, kRows64x64, 64, 64);
-    }
-    if (!dma) offer(3, kTile64, 64, 64);
-    offer(4, kTile64x128[reg], 64, 128);
-    offer(5, kTile128[reg], 128, 128);
-    if (dma) offer(6, kTileMid, 128, 128);
-    if (!dma) offer(7, kTile256x128, 256, 128);
-    offer(8, kTile256[reg], 256, 256);
-    switch (best) {
-        case 0:
+    const auto [kernel, dma] = choose(a, DUAL);
+    switch (kernel) {
+        case FEW1: return launch_few<1, DUAL>(a, s);
+        case FEW2: return launch_few<2, DUAL>(a, s);
+        case FEW4: return launch_few<4, DUAL>(a, s);
+        case FEW8: return launch_few<8, DUAL>(a, s);
+        case ROWS32:
             if constexpr (!DUAL) return launch_rows<32, 32, DUAL>(a, dma, s);
-        case 1: return launch_rows<32, 64, DUAL>(a, dma, s);
-        case 2: return launch_rows<64, 64, DUAL>(a, dma, s);
-        case 3: return go(TypeTag<Flat<64, 64, 32, 64, 2, 2>>{});
-        case 4: return dma ? go(TypeTag<Ring<64, 128, 32, 64, 3>>{}) : go(TypeTag<Flat<64, 128, 32, 64>>{});
-        case 5: return dma ? go(TypeTag<Ring<128, 128, 32, 64, 4>>{}) : go(TypeTag<Flat<128, 128, 32, 64>>{});
-        case 6: return go(TypeTag<TileMid>{});
-        case 7: return go(TypeTag<Flat<256, 128, 64, 64>>{});
-        default: return dma ? go(TypeTag<TileBig>{}) : go(TypeTag<Flat<256, 256, 128, 64>>{});
+        case ROWS64: return launch_rows<32, 64, DUAL>(a, dma, s);
+        case ROWS64X64: return launch_rows<64, 64, DUAL>(a, dma, s);
+        case TILE64: return go(TypeTag<Flat<64, 64, 32, 64, 2, 2>>{});
+        case TILE64X128: return dma ? go(TypeTag<Ring<64, 128, 32, 64, 3>>{}) : go(TypeTag<Flat<64, 128, 32, 64>>{});
+        case TILE128: return dma ? go(TypeTag<Ring<128, 128, 32, 64, 4>>{}) : go(TypeTag<Flat<128, 128, 32, 64>>{});
+        case TILE_MID: return go(TypeTag<TileMid>{});
+        case TILE256X128: return go(TypeTag<Flat<256, 128, 64, 64>>{});
+        case TILE256: return dma ? go(TypeTag<TileBig>{}) : go(TypeTag<Flat<256, 256, 128, 64>>{});
+        case TILE_SHORT: return go(TypeTag<TileShort>{});
+        default: return go(TypeTag<TileReg64>{});
     }
 }
 

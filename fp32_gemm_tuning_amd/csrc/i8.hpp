@@ -68,6 +68,7 @@ size_t norm_part_bytes(int dtype, int64_t M, int64_t K);
 hipError_t launch_norm_bwd(int dtype, const NormBwdArgs& a, hipStream_t s);
 // i8.hip
 int check_i8(const I8Args& a, bool dual);
+const char* i8_kernel_name(const I8Args& a, bool dual);   // of the kernel that launch_i8 launches
 hipError_t launch_i8(const I8Args& a, bool dual, hipStream_t s);
 
 }  // namespace sgemm

@@ -1,10 +1,13 @@
 // C-ABI entry points of include/sgemm_f32_i8.h: argument checks, quick
-// returns and the launches.
+// returns and the launches; and the name of the kernel that a product takes
+// (include/sgemm_f32_probe.h).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 
 #include "i8.hpp"
+
+#include "sgemm_f32_probe.h"
 
 namespace sgemm {
 namespace {
@@ -52,9 +55,11 @@ int check_total(int dtype, int64_t M, int64_t K, const void* H, int64_t ldh) {
     return 0;
 }
 
-int run_i8(int dtype, bool dual, int act, int64_t M, int64_t F, int64_t K, const int8_t* X, int64_t ldx,
-           const float* Sx, const int8_t* W0, int64_t ldw0, const float* S0, const int8_t* W1, int64_t ldw1,
-           const float* S1, void* Y, int64_t ldy, void* stream) {
+// The checks of a product; `a` is filled where 0 is returned and there is something to launch.
+int check_product(int dtype, bool dual, int act, int64_t M, int64_t F, int64_t K, const int8_t* X, int64_t ldx,
+                  const float* Sx, const int8_t* W0, int64_t ldw0, const float* S0, const int8_t* W1, int64_t ldw1,
+                  const float* S1, void* Y, int64_t ldy, I8Args& a) {
+    a.Y = nullptr;
     int rc = check_sizes(dtype, 0, 0, 0);
     if (rc == 0 && dual && (act < SGEMM_F32_ACT_SILU || act > SGEMM_F32_ACT_RELU)) rc = -18;
     if (rc == 0) rc = check_sizes(dtype, M, F, K);
@@ -75,10 +80,15 @@ int run_i8(int dtype, bool dual, int act, int64_t M, int64_t F, int64_t K, const
     if (short_ld(ldy, F)) return -11;
     if (!out) return 0;
     if (too_large(M, F, K) || K > kMaxSum) return SGEMM_F32_ERR_TOO_LARGE;
-    const I8Args a = {X, Sx, {W0, W1}, {S0, S1}, Y, ldx, {ldw0, ldw1}, ldy, (int32_t)M, (int32_t)F, (int32_t)K,
-                      dtype, act};
-    rc = check_i8(a, dual);
-    if (rc) return rc;
+    a = I8Args{X, Sx, {W0, W1}, {S0, S1}, Y, ldx, {ldw0, ldw1}, ldy, (int32_t)M, (int32_t)F, (int32_t)K, dtype, act};
+    return check_i8(a, dual);
+}
+int run_i8(int dtype, bool dual, int act, int64_t M, int64_t F, int64_t K, const int8_t* X, int64_t ldx,
+           const float* Sx, const int8_t* W0, int64_t ldw0, const float* S0, const int8_t* W1, int64_t ldw1,
+           const float* S1, void* Y, int64_t ldy, void* stream) {
+    I8Args a;
+    const int rc = check_product(dtype, dual, act, M, F, K, X, ldx, Sx, W0, ldw0, S0, W1, ldw1, S1, Y, ldy, a);
+    if (rc || a.Y == nullptr) return rc;
     return status(launch_i8(a, dual, reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -204,6 +214,17 @@ SGEMM_F32_API int sgemm_f32_i8_glu(int dtype, int act, int64_t M, int64_t F, int
                                    const float* Sg, const int8_t* Wu, int64_t ldwu, const float* Su,
                                    void* H, int64_t ldh, void* stream) {
     return run_i8(dtype, true, act, M, F, K, X, ldx, Sx, Wg, ldwg, Sg, Wu, ldwu, Su, H, ldh, stream);
+}
+
+SGEMM_F32_API const char* sgemm_f32_i8_kernel(int gated, int64_t M, int64_t F, int64_t K, const int8_t* X,
+                                              int64_t ldx, const int8_t* Wg, int64_t ldwg, const int8_t* Wu,
+                                              int64_t ldwu) {
+    // (the choice does not look at the type, the scales or the output: any that pass the checks)
+    alignas(16) static float any[1];
+    I8Args a;
+    const int rc = check_product(SGEMM_F32_DTYPE_F32, gated != 0, SGEMM_F32_ACT_SILU, M, F, K, X, ldx, any, Wg, ldwg, any,
+                                 gated ? Wu : nullptr, gated ? ldwu : 1, any, any, F > 1 ? F : 1, a);
+    return rc || a.Y == nullptr ? nullptr : i8_kernel_name(a, gated != 0);
 }
 
 }  // extern "C"

@@ -12,6 +12,8 @@ or raw device addresses as ints; they return the C status code):
     sgemm_f32_i8_dequantize(dtype, M, K, Q, ldq, S, X, ldx, stream=None)
     sgemm_f32_i8(dtype, M, F, K, X, ldx, Sx, W, ldw, Sw, Y, ldy, stream=None)
     sgemm_f32_i8_glu(dtype, act, M, F, K, X, ldx, Sx, Wg, ldwg, Sg, Wu, ldwu, Su, H, ldh, stream=None)
+and, of include/sgemm_f32_probe.h, the name of the kernel that a product takes (None: none):
+    sgemm_f32_i8_kernel(gated, M, F, K, X, ldx, Wg, ldwg, Wu=None, ldwu=1)
 
 Tensor helpers, with ffn.py's rules for tensors, streams, errors and allocated outputs
 (norm weights, scales and rstd are 1-D and contiguous):
@@ -54,6 +56,10 @@ for _name, _types in _SIGNATURES.items():
     getattr(_lib, _name).argtypes = _types
     getattr(_lib, _name).restype = _c
     _entries[_name] = getattr(_lib, _name)
+
+
+_lib.sgemm_f32_i8_kernel.argtypes = [_c, _i, _i, _i] + 3 * _m
+_lib.sgemm_f32_i8_kernel.restype = ctypes.c_char_p
 
 
 # --------------------------------------------------------------------------
@@ -99,6 +105,11 @@ def sgemm_f32_i8(dtype, M, F, K, X, ldx, Sx, W, ldw, Sw, Y, ldy, stream=None) ->
 def sgemm_f32_i8_glu(dtype, act, M, F, K, X, ldx, Sx, Wg, ldwg, Sg, Wu, ldwu, Su, H, ldh, stream=None) -> int:
     return _lib.sgemm_f32_i8_glu(dtype, act, M, F, K, _ptr(X), ldx, _ptr(Sx), _ptr(Wg), ldwg, _ptr(Sg), _ptr(Wu),
                                  ldwu, _ptr(Su), _ptr(H), ldh, _stream(stream, H, X))
+
+
+def sgemm_f32_i8_kernel(gated, M, F, K, X, ldx, Wg, ldwg, Wu=None, ldwu=1):
+    name = _lib.sgemm_f32_i8_kernel(int(gated), M, F, K, _ptr(X), ldx, _ptr(Wg), ldwg, _ptr(Wu), ldwu)
+    return None if name is None else name.decode()
 
 
 # --------------------------------------------------------------------------

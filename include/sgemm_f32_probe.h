@@ -5,7 +5,8 @@
  * card ("100 Days of GPU, Day 44", opening paragraphs) and place kernels under
  * the roofline's flat compute ceiling ("Optimizing Matrix Multiply on CUDA,
  * Part 1", "The Roofline"). This probe measures that ceiling on MI355X for
- * the instruction families the SGEMM kernels use.
+ * the instruction families the SGEMM kernels use. Beside it, the name of the
+ * kernel that a product of matrices in 8 bits takes.
  */
 #ifndef SGEMM_F32_PROBE_H
 #define SGEMM_F32_PROBE_H
@@ -45,6 +46,15 @@ SGEMM_F32_API int sgemm_f32_peak_probe(int kind, int workgroups, int iters, floa
  * runtime reports them. Returns 0, -1 if a pointer is NULL,
  * SGEMM_F32_ERR_DEVICE, or a positive hipError_t. */
 SGEMM_F32_API int sgemm_f32_clock_rates(int *wall_khz, int *max_sclk_khz);
+
+/* The kernel that sgemm_f32_i8 (gated = 0; Wu and ldwu are not looked at) or
+ * sgemm_f32_i8_glu (gated != 0) launches for these sizes and operands, so that a
+ * test or a timing can say what it reached: a static name, or NULL where the
+ * call launches nothing or is refused. Host only: of the addresses, their
+ * alignment is looked at. */
+SGEMM_F32_API const char *sgemm_f32_i8_kernel(int gated, int64_t M, int64_t F, int64_t K, const int8_t *X,
+                                              int64_t ldx, const int8_t *Wg, int64_t ldwg,
+                                              const int8_t *Wu, int64_t ldwu);
 
 #ifdef __cplusplus
 }
