@@ -194,7 +194,9 @@ __global__ __launch_bounds__(256) void k_norm_dw_long(NormBwdArgs a, int rows) {
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_dw_sum(NormBwdArgs a, int parts) {
     __shared__ float red[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = blockIdx.x * 64 + lane;
+    // (blockIdx.y: rows of 2^28 and more have more blocks of columns than one line of the grid has threads for)
+    const int block = blockIdx.y * gridDim.x + blockIdx.x;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = block * 64 + lane;
     float s = 0.0f;
     if (k < a.K) {
 #pragma unroll 8
@@ -290,7 +292,9 @@ hipError_t launch_norm_bwd(int dtype, const NormBwdArgs& a, hipStream_t s) {
             e = hipGetLastError();
         }
         if (e == hipSuccess && a.dW != nullptr) {
-            hipLaunchKernelGGL((k_norm_dw_sum<T>), dim3((unsigned)((a.K + 63) / 64)), dim3(1024), 0, s, a, (int)parts);
+            const int blocks = (a.K + 63) / 64, line = 1 << 20, lines = (blocks + line - 1) / line;
+            hipLaunchKernelGGL((k_norm_dw_sum<T>), dim3((unsigned)(lines > 1 ? line : blocks), (unsigned)lines), dim3(1024), 0,
+                               s, a, (int)parts);
             e = hipGetLastError();
         }
         return e;
