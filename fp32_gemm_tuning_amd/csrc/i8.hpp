@@ -32,7 +32,7 @@ struct NormBwdArgs {
     const void* dH;     // null: none
     void* dX;           // null: not wanted
     void* dW;           // null: not wanted
-    float* part;        // partial sums of dW, norm_parts(M, K) rows of K
+    float* part;        // partial sums of dW, rows of K (norm_part_bytes of them)
     int64_t lddy, ldh, lddh, lddx;
     int32_t M, K;
 };

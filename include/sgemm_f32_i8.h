@@ -41,7 +41,9 @@
  * int8. H is rounded to the type, and everything after it uses the rounded one, so that the
  * backward pass sees what the forward pass did. Sums over a row or over rows are held in FP32
  * (squares next to the ends of its range are summed times a power of two); each output is
- * rounded to the type once, from FP32.
+ * rounded to the type once, from FP32. The backward pass forms dY W and dY W N in FP32, so these have
+ * to lie in its range. A root mean square above 2^126 has an rstd below FP32's normal numbers, whose
+ * rounding (2^-22 at most, relative, not 2^-24) is in what it scales.
  *
  * Infinities and NaN stay in their rows (dW: in their columns): a row of H that holds an infinity has
  * rstd = 0, and Y = 0 but for the infinity, where it is NaN; one that holds NaN is NaN. With eps = 0 a row
