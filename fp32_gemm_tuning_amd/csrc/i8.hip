@@ -480,10 +480,10 @@ __global__ __launch_bounds__(256) void k_i8_few(I8Args a) {
 
 // Few rows: the weights' bytes are the work. A workgroup takes BM rows of X and BN weight rows (DUAL: of two
 // matrices in blocks of 32); its KW waves take K's slices in turn, each with a ring of LDS stages of its own, so
-// no wave waits for another before the sums are added. Bound by the weights' way to the units: 16 rows of 8192 x 8192
-// 17.7 us (3.8 TB/s) cached and 18.2 from memory, where rows a power of two apart meet in the same few channels:
-// with 128 bytes more between them 14.8 and 15.5; 64 of 4096 x 4096 6.8 and 8.8. Through registers, gated 33 of 4091 x
-// 4092, 12.7.
+// no wave waits for another before the sums are added. Bound by the weights' way to the units: 16 rows of 8192 x
+// 8192 17.7 us (3.8 TB/s) cached and 18.2 from memory, where rows a power of two apart meet in the same few
+// channels: with 128 bytes more between them 14.8 and 15.5; 64 of 4096 x 4096 6.8 and 8.8. Through registers, gated
+// 33 of 4091 x 4092, 12.7.
 constexpr int KW = 4;
 template <int BM, int BN, bool DUAL, bool DMA>
 __global__ __launch_bounds__(KW * 64) void k_i8_rows(I8Args a) {
@@ -638,16 +638,16 @@ int check_i8(const I8Args& a, bool dual) {
     return tiles <= max_workgroups(512) && zeros <= max_workgroups(256) ? 0 : SGEMM_F32_ERR_TOO_LARGE;
 }
 
-// Times that the choice of a kernel goes by, in microseconds, measured on MI355X with operands in the caches (products of 16
-// to 4096 rows, 300 to 8192 features and 777 to 8192 k): a call takes about
+// Times that the choice of a kernel goes by, in microseconds, measured on MI355X with operands in the caches
+// (products of 16 to 4096 rows, 300 to 8192 features and 777 to 8192 k): a call takes about
 //     fixed + rounds * each + slices max(alone, rounds * busy)
 // for `rounds` tiles on a compute unit, with `alone` a slice of 128 k where tiles are few and `busy` a tile's share
 // of a unit's slice where every unit has one or more; a workgroup of the rows' kernel has its unit to itself, and its
 // start and its sums (`each`) with it. What bounds a lone tile's slice is its bytes: a unit takes some 70
-// GB/s from the caches, whatever is under way (two to eight slices a workgroup were level). Predictions are off by 15% on
-// the average, and 10% short with weights from memory (22% up to 32 rows); of 104 products of random sizes the
-// choice took 1.9% longer than the best kernel on the average with weights in the caches (at worst 32%) and 1.5% with weights from
-// memory (24%).
+// GB/s from the caches, whatever is under way (two to eight slices a workgroup were level). Predictions are off
+// by 15% on the average, and 10% short with weights from memory (22% up to 32 rows); of 104 products of random
+// sizes the choice took 1.9% longer than the best kernel on the average with weights in the caches (at worst 32%)
+// and 1.5% with weights from memory (24%).
 struct Cost {
     double fixed, each, alone, busy;
     double of(int64_t tiles, int64_t slices) const {

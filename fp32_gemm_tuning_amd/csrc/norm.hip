@@ -127,9 +127,9 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t m, int lane,
 }
 
 // Longer rows: a workgroup each, read from the caches or memory in every pass. Bound by those
-// reads: 512 x 65536 bf16 with a residual 59 us (268 MB, 4.5 TB/s), one row 11. In 8 bits also by the passes' arithmetic, in 64 bits for
-// every type: with a residual 76 us (235 MB, 3.1 TB/s), one row 23; a matrix alone 512 x 53248 bf16 30 (82 MB, 2.7
-// TB/s), FP32 38 (136 MB, 3.6 TB/s).
+// reads: 512 x 65536 bf16 with a residual 59 us (268 MB, 4.5 TB/s), one row 11. In 8 bits also by the passes'
+// arithmetic, in 64 bits for every type: with a residual 76 us (235 MB, 3.1 TB/s), one row 23; a matrix alone 512 x
+// 53248 bf16 30 (82 MB, 2.7 TB/s), FP32 38 (136 MB, 3.6 TB/s).
 constexpr int LONG_NT = 1024;
 template <class T, NormMode MODE>
 __global__ __launch_bounds__(LONG_NT) void k_norm_long(NormArgs a) {

@@ -128,9 +128,9 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 4) void k_norm_bwd(NormB
     }
 }
 
-// dX of longer rows: a workgroup a row, read twice; dW's kernels read dY and H once more. Bound by those reads: 512 x
-// 65536 bf16 with dH and dW 99 us (268 MB read and written once, 2.7 TB/s), 1024 x 28672 97 (2.4 TB/s), one row of 65536 20. In 16 bits
-// this begins at 16385 elements: 1024 x 16384 in registers 32 us, x 16392 58.
+// dX of longer rows: a workgroup a row, read twice; dW's kernels read dY and H once more. Bound by those reads: 512
+// x 65536 bf16 with dH and dW 99 us (268 MB read and written once, 2.7 TB/s), 1024 x 28672 97 (2.4 TB/s), one row of
+// 65536 20. In 16 bits this begins at 16385 elements: 1024 x 16384 in registers 32 us, 1024 x 16392 58.
 constexpr int LONG_NT = 1024;
 template <class T>
 __global__ __launch_bounds__(LONG_NT) void k_norm_dx_long(NormBwdArgs a) {
@@ -190,9 +190,9 @@ __global__ __launch_bounds__(256) void k_norm_dw_long(NormBwdArgs a, int rows) {
 }
 
 // The parts' sums: 64 columns a workgroup, whose sixteen waves take every sixteenth
-// part and meet in their order. Bound by its launch and its loads' latency, eight parts a batch one after the other: 512
-// parts of 8192 4.7 us, 500 of 1531 5.6 in 24 workgroups, as long as the pass before it (one thread a column 61 us for 256
-// parts of 8192).
+// part and meet in their order. Bound by its launch and its loads' latency, eight parts a batch one after the
+// other: 512 parts of 8192 4.7 us, 500 of 1531 5.6 in 24 workgroups, beside 6.3 for the pass before it (one thread a
+// column 61 us for 256 parts of 8192).
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_dw_sum(NormBwdArgs a, int parts) {
     __shared__ float red[16][64];
@@ -295,8 +295,8 @@ hipError_t launch_norm_bwd(int dtype, const NormBwdArgs& a, hipStream_t s) {
         }
         if (e == hipSuccess && a.dW != nullptr) {
             const int blocks = (a.K + 63) / 64, line = 1 << 20, lines = (blocks + line - 1) / line;
-            hipLaunchKernelGGL((k_norm_dw_sum<T>), dim3((unsigned)(lines > 1 ? line : blocks), (unsigned)lines), dim3(1024), 0,
-                               s, a, (int)parts);
+            hipLaunchKernelGGL((k_norm_dw_sum<T>), dim3((unsigned)(lines > 1 ? line : blocks), (unsigned)lines),
+                               dim3(1024), 0, s, a, (int)parts);
             e = hipGetLastError();
         }
         return e;

@@ -151,7 +151,8 @@ def test_scales_that_are_not_ordinary(dev, gated, name, shape):
     # in a tile's columns and rows beside them come from the other form of the product.
     sx, sa = x.scales.clone(), a.scales.clone()
     plain = {t: call(sx, sa, t) for t in ref.DTYPES.values()}
-    cols = {c % F: v for c, v in ((3, 0.0), (5, float("inf")), (40, float("nan")), (F - 2, 2.0 ** 100), (70, 2.0 ** -140))}
+    cols = {c % F: v for c, v in ((3, 0.0), (5, float("inf")), (40, float("nan")), (F - 2, 2.0 ** 100),
+                                  (70, 2.0 ** -140))}
     rows = {} if M < 3 else {1: float("nan"), M - 1: 2.0 ** -100}
     for c, v in cols.items():
         sa[c] = v
